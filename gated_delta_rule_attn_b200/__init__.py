@@ -1,4 +1,5 @@
-"""Causal linear attention (ELU+1 / GLA / gated delta rule) for B200.
+"""Causal linear attention (ELU+1 / GLA / gated delta rule) for B200, the gated
+linear recurrence with a vector state, and the norms around them.
 
 Thin Python binding over the C ABI in ``include/la.h``: it only checks tensor
 properties, allocates outputs with PyTorch and passes pointers, sizes and the
@@ -18,6 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libla_b200.so")
 ABI_VERSION = 3   # LA_ABI_VERSION of include/la.h that these struct layouts follow
 
+GATES = {"value": 0, "logit": 1}
+NORMS = {"layer": 0, "rms": 1}
 RULES = {"elu": 0, "gla": 1, "gdn": 2, "kda": 3}
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_ERR_ALIGNMENT",
@@ -27,7 +30,9 @@ STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_E
 # Symbols include/la.h and include/la_testing.h declare (checked by the CPU test suite).
 EXPORTS = ("la_fwd", "la_fwd_workspace_size", "la_step", "la_fwd_host_staging_size",
            "la_fwd_host", "la_check_device", "la_status_string", "la_last_error_message",
-           "la_abi_version", "la_fwd_noalloc", "la_testing_set_wait_limit")
+           "la_abi_version", "la_fwd_noalloc", "la_testing_set_wait_limit",
+           "la_scan_fwd", "la_scan_bwd", "la_scan_step",
+           "la_norm_fwd", "la_norm_bwd", "la_norm_bwd_workspace_size")
 
 
 class LAError(RuntimeError):
@@ -59,6 +64,40 @@ class StepArgs(ctypes.Structure):
                 ("out_norm", ctypes.c_int32), ("norm_eps", ctypes.c_float), ("norm_w", ctypes.c_void_p)]
 
 
+_U, _I, _L, _V, _F = ctypes.c_uint32, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class ScanFwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _U), ("dtype", _I), ("gate_dtype", _I), ("gate", _I), ("tied", ctypes.c_int32),
+                ("B", _L), ("T", _L), ("D", _L), ("x", _V), ("x_row", _L), ("g", _V), ("g_row", _L),
+                ("h0", _V), ("h", _V), ("h_row", _L), ("h_last", _V), ("cu_seqlens", _V), ("max_seqlen", _L)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _U), ("dtype", _I), ("gate_dtype", _I), ("gate", _I), ("tied", ctypes.c_int32),
+                ("B", _L), ("T", _L), ("D", _L), ("x", _V), ("x_row", _L), ("g", _V), ("g_row", _L),
+                ("h", _V), ("h_row", _L), ("dh", _V), ("dh_row", _L), ("h0", _V), ("dh_last", _V),
+                ("dx", _V), ("dx_row", _L), ("dg", _V), ("dg_row", _L), ("dh0", _V),
+                ("cu_seqlens", _V), ("max_seqlen", _L)]
+
+
+class ScanStepArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _U), ("dtype", _I), ("gate_dtype", _I), ("gate", _I), ("tied", ctypes.c_int32),
+                ("N", _L), ("D", _L), ("x", _V), ("x_row", _L), ("g", _V), ("g_row", _L), ("state", _V),
+                ("h", _V), ("h_row", _L)]
+
+
+class NormFwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _U), ("dtype", _I), ("kind", _I), ("R", _L), ("D", _L), ("x", _V), ("x_row", _L),
+                ("w", _V), ("b", _V), ("eps", _F), ("y", _V), ("y_row", _L), ("mean", _V), ("rstd", _V)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [("struct_size", _U), ("dtype", _I), ("kind", _I), ("R", _L), ("D", _L), ("x", _V), ("x_row", _L),
+                ("dy", _V), ("dy_row", _L), ("w", _V), ("mean", _V), ("rstd", _V), ("dx", _V), ("dx_row", _L),
+                ("dw", _V), ("db", _V), ("workspace", _V), ("workspace_bytes", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -83,8 +122,13 @@ def lib():
         L.la_status_string.argtypes = [ctypes.c_int]
         L.la_status_string.restype = ctypes.c_char_p
         L.la_last_error_message.restype = ctypes.c_char_p
+        for f, args in ((L.la_scan_fwd, ScanFwdArgs), (L.la_scan_bwd, ScanBwdArgs), (L.la_scan_step, ScanStepArgs),
+                        (L.la_norm_fwd, NormFwdArgs), (L.la_norm_bwd, NormBwdArgs)):
+            f.argtypes = [ctypes.POINTER(args), P]
+        L.la_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(NormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]
         for f in (L.la_fwd, L.la_fwd_workspace_size, L.la_step, L.la_fwd_host_staging_size,
-                  L.la_fwd_host, L.la_check_device, L.la_fwd_noalloc):
+                  L.la_fwd_host, L.la_check_device, L.la_fwd_noalloc, L.la_scan_fwd, L.la_scan_bwd,
+                  L.la_scan_step, L.la_norm_fwd, L.la_norm_bwd, L.la_norm_bwd_workspace_size):
             f.restype = ctypes.c_int
         L.la_abi_version.restype = ctypes.c_int
         if L.la_abi_version() != ABI_VERSION:
@@ -281,6 +325,261 @@ def fwd_host(rule: str, q, k, v, g=None, beta=None, S0=None, z0=None, eps: float
     _check(lib().la_fwd_host(ctypes.byref(a), ctypes.c_void_p(staging.data_ptr()),
                              staging.numel(), _stream_handle(stream)))
     return o, S_out, z_out
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence and row norms.
+# ---------------------------------------------------------------------------
+def _tokens(t, name, lead, tail, dtype, device):
+    """The distance in elements between the rows of ``t``, a tensor of shape
+    ``lead + tail`` whose trailing dims are dense and whose leading dims are one
+    axis of equally spaced rows (0 when the whole tensor is dense)."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != lead + tail:
+        raise ValueError(f"{name} must have shape {tuple(lead + tail)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    size, stride = t.shape, t.stride()
+    n, D = len(lead), 1
+    for i in range(len(size) - 1, n - 1, -1):
+        if size[i] != 1 and stride[i] != D:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        D *= size[i]
+    row, step = 0, 0
+    for i in range(n - 1, -1, -1):
+        if size[i] == 1:
+            continue
+        if not row:
+            row = step = stride[i]
+            if row < D:
+                raise ValueError(f"{name}: rows overlap (a broadcast tensor has to be made contiguous)")
+        elif stride[i] != step:
+            raise ValueError(f"{name}: the leading dims must be one axis of equally spaced rows")
+        step *= size[i]
+    return row
+
+
+def _dense(t, name, shape, device, dtype=torch.float32):
+    """Address of a dense fp32 tensor of that shape, or None."""
+    if t is None:
+        return None
+    if t.device != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+class _On:
+    """The device and the stream of a call: the current stream of the tensors'
+    device, or ``stream``.  Inside, new tensors belong to that stream; the memory
+    of ``tensors`` is kept until the work queued on a given ``stream`` is done."""
+
+    def __init__(self, device, stream, *tensors):
+        if device.type != "cuda":
+            raise ValueError("the tensors must be on a CUDA device")
+        self.ctx = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("stream belongs to another device than the tensors")
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.device(device)
+        self.device, self.stream, self.tensors = device, stream, tensors
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _choice(table, key, name):
+    try:
+        return table[key]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(map(str, table))}, got {key!r}") from None
+
+
+def _scan_shape(g, cu_seqlens, max_seqlen):
+    """(lead, tail, sequences, D, address of cu_seqlens, max_seqlen) of token tensors like g."""
+    if g.dim() < 3:
+        raise ValueError("token tensors are [B, T, D] or [B, T, H, d]")
+    lead, tail = g.shape[:2], g.shape[2:]
+    D = 1
+    for n in tail:
+        D *= n
+    if cu_seqlens is None:
+        if max_seqlen is not None:
+            raise ValueError("max_seqlen goes with cu_seqlens")
+        return lead, tail, lead[0], D, None, 0
+    if lead[0] != 1:
+        raise ValueError("packed sequences take token tensors as [1, T, ...]")
+    if cu_seqlens.dtype is not torch.int64 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a 1-D int64 tensor of at least 2 offsets")
+    if max_seqlen is None:
+        raise ValueError("packed sequences need max_seqlen")
+    return (lead, tail, cu_seqlens.numel() - 1, D,
+            _dense(cu_seqlens, "cu_seqlens", cu_seqlens.shape, g.device, torch.int64), int(max_seqlen))
+
+
+def scan_fwd(x, g, h0=None, gate: str = "value", tied: bool = False, h=None, h_last=None,
+             want_state: bool = True, cu_seqlens=None, max_seqlen=None, stream=None):
+    """Gated linear recurrence ``h_t = a_t h_{t-1} + u_t`` per channel (la_scan_fwd
+    in la.h): returns (h, h_last), on the current stream of the tensors' device.
+
+    ``x``, ``g`` [B, T, D] or [B, T, H, d], fp32 or bf16 each; their rows may be
+    slices of wider ones.  ``gate``: ``"value"`` (a = g) or ``"logit"``
+    (a = sigmoid(g)).  ``tied``: u = (1 - a) x instead of x.  ``h0``, ``h_last``
+    fp32 [B, D] ([B, H, d]); ``h_last`` may be ``h0``.  ``cu_seqlens`` /
+    ``max_seqlen``: packed sequences as for ``fwd`` (states [sequences, ...])."""
+    dev = x.device
+    lead, tail, N, D, cu, ms = _scan_shape(g, cu_seqlens, max_seqlen)
+    gt, dt = _choice(GATES, gate, "gate"), _choice(DTYPES, x.dtype, "x.dtype")
+    gd = _choice(DTYPES, g.dtype, "g.dtype")
+    xr, gr = _tokens(x, "x", lead, tail, x.dtype, dev), _tokens(g, "g", lead, tail, g.dtype, dev)
+    state = (N,) + tuple(tail)
+    with _On(dev, stream, x, g, h0, h, h_last, cu_seqlens) as st:
+        if h is None:
+            h = torch.empty(lead + tail, dtype=x.dtype, device=dev)
+        if h_last is None and want_state:
+            h_last = torch.empty(state, dtype=torch.float32, device=dev)
+        a = ScanFwdArgs(ctypes.sizeof(ScanFwdArgs), dt, gd, gt, 1 if tied else 0, N, lead[1], D,
+                        x.data_ptr(), xr, g.data_ptr(), gr, _dense(h0, "h0", state, dev), h.data_ptr(),
+                        _tokens(h, "h", lead, tail, x.dtype, dev), _dense(h_last, "h_last", state, dev), cu, ms)
+        _check(lib().la_scan_fwd(ctypes.byref(a), st))
+    return h, h_last
+
+
+def scan_bwd(g, h, dh, x=None, h0=None, dh_last=None, gate: str = "value", tied: bool = False,
+             dx=None, dg=None, dh0=None, want_state: bool = True, cu_seqlens=None, max_seqlen=None, stream=None):
+    """Gradients of ``scan_fwd`` (la_scan_bwd in la.h): returns (dx, dg, dh0).
+
+    ``h`` is what ``scan_fwd`` returned, ``dh`` the gradient of h, ``dh_last`` that
+    of h_last (fp32, or None for zero).  ``x`` is needed for a tied input only.
+    dx has the type of dh, dg that of g, dh0 is fp32."""
+    dev = g.device
+    lead, tail, N, D, cu, ms = _scan_shape(g, cu_seqlens, max_seqlen)
+    gt, dt = _choice(GATES, gate, "gate"), _choice(DTYPES, dh.dtype, "dh.dtype")
+    gd = _choice(DTYPES, g.dtype, "g.dtype")
+    if tied and x is None:
+        raise ValueError("a tied input's gradient needs x")
+    xr = _tokens(x, "x", lead, tail, dh.dtype, dev) if tied else 0
+    gr, hr = _tokens(g, "g", lead, tail, g.dtype, dev), _tokens(h, "h", lead, tail, dh.dtype, dev)
+    dhr = _tokens(dh, "dh", lead, tail, dh.dtype, dev)
+    state = (N,) + tuple(tail)
+    with _On(dev, stream, x, g, h, dh, h0, dh_last, dx, dg, dh0, cu_seqlens) as st:
+        if dx is None:
+            dx = torch.empty(lead + tail, dtype=dh.dtype, device=dev)
+        if dg is None:
+            dg = torch.empty(lead + tail, dtype=g.dtype, device=dev)
+        if dh0 is None and want_state:
+            dh0 = torch.empty(state, dtype=torch.float32, device=dev)
+        a = ScanBwdArgs(ctypes.sizeof(ScanBwdArgs), dt, gd, gt, 1 if tied else 0, N, lead[1], D,
+                        x.data_ptr() if tied else None, xr, g.data_ptr(), gr, h.data_ptr(), hr,
+                        dh.data_ptr(), dhr, _dense(h0, "h0", state, dev), _dense(dh_last, "dh_last", state, dev),
+                        dx.data_ptr(), _tokens(dx, "dx", lead, tail, dh.dtype, dev),
+                        dg.data_ptr(), _tokens(dg, "dg", lead, tail, g.dtype, dev),
+                        _dense(dh0, "dh0", state, dev), cu, ms)
+        _check(lib().la_scan_bwd(ctypes.byref(a), st))
+    return dx, dg, dh0
+
+
+def scan_step(x, g, state, gate: str = "value", tied: bool = False, h=None, stream=None):
+    """One token of the recurrence per sequence: ``state`` (fp32 [N, D] or
+    [N, H, d]) is updated in place, the new state rounded to x's type is returned."""
+    dev = x.device
+    if x.dim() < 2:
+        raise ValueError("x and g are [N, D] or [N, H, d]")
+    lead, tail = x.shape[:1], x.shape[1:]
+    D = 1
+    for n in tail:
+        D *= n
+    gt, dt = _choice(GATES, gate, "gate"), _choice(DTYPES, x.dtype, "x.dtype")
+    gd = _choice(DTYPES, g.dtype, "g.dtype")
+    xr, gr = _tokens(x, "x", lead, tail, x.dtype, dev), _tokens(g, "g", lead, tail, g.dtype, dev)
+    if state is None:
+        raise ValueError("state is needed")
+    with _On(dev, stream, x, g, state, h) as st:
+        if h is None:
+            h = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        a = ScanStepArgs(ctypes.sizeof(ScanStepArgs), dt, gd, gt, 1 if tied else 0, lead[0], D, x.data_ptr(), xr,
+                         g.data_ptr(), gr, _dense(state, "state", x.shape, dev), h.data_ptr(),
+                         _tokens(h, "h", lead, tail, x.dtype, dev))
+        _check(lib().la_scan_step(ctypes.byref(a), st))
+    return h
+
+
+def norm_fwd(x, w=None, b=None, kind: str = "layer", eps: float = 1e-6, y=None, want_stats: bool = True, stream=None):
+    """Layer norm (``kind="layer"``) or RMS norm (``"rms"``) over the last dim of
+    ``x`` (la_norm_fwd in la.h): returns (y, mean, rstd), the statistics fp32 of
+    the leading shape (mean is None for an RMS norm; both are None without
+    ``want_stats``).  ``w``, ``b`` fp32 [D] or None.  The leading dims must be one
+    axis of equally spaced rows."""
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dim")
+    lead, tail = x.shape[:-1], x.shape[-1:]
+    kd, dt = _choice(NORMS, kind, "kind"), _choice(DTYPES, x.dtype, "x.dtype")
+    xr = _tokens(x, "x", lead, tail, x.dtype, dev)
+    with _On(dev, stream, x, w, b, y) as st:
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        mean = rstd = None
+        if want_stats:
+            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+            if kd == 0:
+                mean = torch.empty(lead, dtype=torch.float32, device=dev)
+        a = NormFwdArgs(ctypes.sizeof(NormFwdArgs), dt, kd, lead.numel(), tail[0], x.data_ptr(), xr,
+                        _dense(w, "w", tail, dev), _dense(b, "b", tail, dev), eps, y.data_ptr(),
+                        _tokens(y, "y", lead, tail, x.dtype, dev),
+                        mean.data_ptr() if mean is not None else None, rstd.data_ptr() if want_stats else None)
+        _check(lib().la_norm_fwd(ctypes.byref(a), st))
+    return y, mean, rstd
+
+
+def norm_bwd(dy, x, rstd, mean=None, w=None, kind: str = "layer", dx=None, want_dw: bool = True,
+             want_db: bool = True, stream=None):
+    """Gradients of ``norm_fwd`` (la_norm_bwd in la.h): returns (dx, dw, db), dw and
+    db fp32 [D] (None where not wanted).  ``rstd`` and ``mean`` (layer only) are
+    what ``norm_fwd`` returned.  The partial sums' scratch is allocated for the
+    call, so calls on different streams and captured graphs share none."""
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dim")
+    lead, tail = x.shape[:-1], x.shape[-1:]
+    kd, dt = _choice(NORMS, kind, "kind"), _choice(DTYPES, x.dtype, "x.dtype")
+    xr, dyr = _tokens(x, "x", lead, tail, x.dtype, dev), _tokens(dy, "dy", lead, tail, x.dtype, dev)
+    if rstd is None or (kd == 0) != (mean is not None):
+        raise ValueError("rstd is needed, and mean for a layer norm only")
+    with _On(dev, stream, dy, x, rstd, mean, w, dx) as st:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dw = torch.empty(tail, dtype=torch.float32, device=dev) if want_dw else None
+        db = torch.empty(tail, dtype=torch.float32, device=dev) if want_db else None
+        a = NormBwdArgs(ctypes.sizeof(NormBwdArgs), dt, kd, lead.numel(), tail[0], x.data_ptr(), xr,
+                        dy.data_ptr(), dyr, _dense(w, "w", tail, dev), _dense(mean, "mean", lead, dev),
+                        _dense(rstd, "rstd", lead, dev), dx.data_ptr(),
+                        _tokens(dx, "dx", lead, tail, x.dtype, dev),
+                        dw.data_ptr() if want_dw else None, db.data_ptr() if want_db else None, None, 0)
+        if want_dw or want_db:
+            n = ctypes.c_size_t()
+            _check(lib().la_norm_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+            if n.value:
+                ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
+                a.workspace, a.workspace_bytes = ws.data_ptr(), n.value
+        _check(lib().la_norm_bwd(ctypes.byref(a), st))
+    return dx, dw, db
 
 
 def check_device(stream=None) -> int:

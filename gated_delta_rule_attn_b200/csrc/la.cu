@@ -7,6 +7,8 @@
 // la_step always uses the recurrent kernel with T = 1 and the state in place.
 // With out_norm set, a second pass normalises each (token, head) row of o
 // (out_norm.cuh).
+// la_scan_* run the vector-state recurrence (scan.cuh), la_norm_* the row norms
+// (norm.cuh).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -15,6 +17,7 @@
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -24,6 +27,8 @@
 #include "recurrent.cuh"
 #include "chunk_tc.cuh"
 #include "out_norm.cuh"
+#include "scan.cuh"
+#include "norm.cuh"
 
 namespace {
 
@@ -564,6 +569,218 @@ la_status la_fwd_host(const la_fwd_args *h_in, void *staging, size_t staging_byt
     }
     cudaError_t e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return fail(LA_ERR_CUDA, std::string("sync: ") + cudaGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Gated linear recurrence and row norms.
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// A copy of the caller's struct; every field is required (first version).
+template <typename A>
+la_status load_args(const A *in, A *out) {
+    if (!in) return fail(LA_ERR_INVALID_ARG, "args is NULL");
+    if (in->struct_size < sizeof(A)) return fail(LA_ERR_INVALID_ARG, "struct_size is smaller than the argument struct");
+    *out = *in;
+    return LA_OK;
+}
+
+// 0 means dense; rows may not overlap.
+la_status row_stride(int64_t *row, int64_t D, const char *name) {
+    if (*row == 0) *row = D;
+    if (*row < D) return fail(LA_ERR_INVALID_ARG, std::string(name) + " must be 0 or at least D");
+    return LA_OK;
+}
+
+la_status validate_scan(la_dtype dtype, la_dtype gate_dtype, la_gate gate, int32_t tied, int64_t B, int64_t T,
+                        int64_t D, const int64_t *cu, int64_t max_seqlen) {
+    if ((dtype != LA_F32 && dtype != LA_BF16) || (gate_dtype != LA_F32 && gate_dtype != LA_BF16))
+        return fail(LA_ERR_INVALID_ARG, "dtype and gate_dtype must be LA_F32 or LA_BF16");
+    if (gate != LA_GATE_VALUE && gate != LA_GATE_LOGIT)
+        return fail(LA_ERR_INVALID_ARG, "gate must be LA_GATE_VALUE or LA_GATE_LOGIT");
+    if (tied != 0 && tied != 1) return fail(LA_ERR_INVALID_ARG, "tied must be 0 or 1");
+    if (B < 1 || T < 0 || D < 1) return fail(LA_ERR_INVALID_ARG, "need at least one sequence, T >= 0 and D >= 1");
+    if ((double)B * (double)D > 2.0e9 || (double)B * (double)(T > 0 ? T : 1) * (double)D > 1.0e18)
+        return fail(LA_ERR_INVALID_ARG, "problem too large");
+    if (cu) {
+        if (!aligned_to(cu, 8)) return fail(LA_ERR_ALIGNMENT, "cu_seqlens must be 8-byte aligned");
+        if (max_seqlen < 0 || max_seqlen > T)
+            return fail(LA_ERR_INVALID_ARG, "packed sequences need 0 <= max_seqlen <= T");
+    }
+    return LA_OK;
+}
+
+la_status elem_aligned(std::initializer_list<const void *> ps, la_dtype t) {
+    for (const void *p : ps)
+        if (!aligned_to(p, elem_size(t)))
+            return fail(LA_ERR_ALIGNMENT, "a device pointer is not aligned to its element type");
+    return LA_OK;
+}
+
+template <la::ScanOp OP>
+la_status launch_scan_call(const la::ScanParams &p, la_dtype dt, la_dtype gt, bool logit, bool tied, void *stream) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    using bf = __nv_bfloat16;
+    const cudaError_t e = dt == LA_BF16 ? (gt == LA_BF16 ? la::launch_scan<OP, bf, bf>(p, logit, tied, st)
+                                                         : la::launch_scan<OP, bf, float>(p, logit, tied, st))
+                                        : (gt == LA_BF16 ? la::launch_scan<OP, float, bf>(p, logit, tied, st)
+                                                         : la::launch_scan<OP, float, float>(p, logit, tied, st));
+    if (e != cudaSuccess) return fail(LA_ERR_CUDA, std::string("scan launch: ") + cudaGetErrorString(e));
+    return ok();
+}
+
+la_status validate_rows(la_dtype dtype, la_norm_kind kind, int64_t R, int64_t D) {
+    if (dtype != LA_F32 && dtype != LA_BF16) return fail(LA_ERR_INVALID_ARG, "dtype must be LA_F32 or LA_BF16");
+    if (kind != LA_NORM_LAYER && kind != LA_NORM_RMS)
+        return fail(LA_ERR_INVALID_ARG, "kind must be LA_NORM_LAYER or LA_NORM_RMS");
+    if (R < 0 || D < 1) return fail(LA_ERR_INVALID_ARG, "need R >= 0 and D >= 1");
+    if (D > LA_NORM_MAX_D) return fail(LA_ERR_UNSUPPORTED, "rows of more than LA_NORM_MAX_D elements have no kernel");
+    if ((double)R * (double)D > 1.0e18) return fail(LA_ERR_INVALID_ARG, "problem too large");
+    return LA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+la_status la_scan_fwd(const la_scan_fwd_args *in, void *stream) {
+    la_scan_fwd_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    r = validate_scan(a.dtype, a.gate_dtype, a.gate, a.tied, a.B, a.T, a.D, a.cu_seqlens, a.max_seqlen);
+    if (r != LA_OK) return r;
+    if (a.T > 0 && (!a.x || !a.g || !a.h)) return fail(LA_ERR_INVALID_ARG, "x, g and h must be non-NULL when T > 0");
+    if ((r = row_stride(&a.x_row, a.D, "x_row")) != LA_OK || (r = row_stride(&a.g_row, a.D, "g_row")) != LA_OK ||
+        (r = row_stride(&a.h_row, a.D, "h_row")) != LA_OK)
+        return r;
+    if ((r = elem_aligned({a.x, a.h}, a.dtype)) != LA_OK || (r = elem_aligned({a.g}, a.gate_dtype)) != LA_OK ||
+        (r = elem_aligned({a.h0, a.h_last}, LA_F32)) != LA_OK)
+        return r;
+    la::ScanParams p{};
+    p.B = a.B; p.T = a.T; p.D = a.D;
+    p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
+    p.h0 = a.h0; p.h = a.h; p.h_row = a.h_row; p.h_last = a.h_last;
+    p.cu_seqlens = a.cu_seqlens; p.max_seqlen = a.max_seqlen;
+    return launch_scan_call<la::ScanOp::kFwd>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+}
+
+la_status la_scan_bwd(const la_scan_bwd_args *in, void *stream) {
+    la_scan_bwd_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    r = validate_scan(a.dtype, a.gate_dtype, a.gate, a.tied, a.B, a.T, a.D, a.cu_seqlens, a.max_seqlen);
+    if (r != LA_OK) return r;
+    if (a.T > 0 && (!a.g || !a.h || !a.dh || !a.dx || !a.dg))
+        return fail(LA_ERR_INVALID_ARG, "g, h, dh, dx and dg must be non-NULL when T > 0");
+    if (a.T > 0 && a.tied && !a.x) return fail(LA_ERR_INVALID_ARG, "a tied input's gradient needs x");
+    if (!a.tied && a.x) return fail(LA_ERR_INVALID_ARG, "x is read for a tied input only: it must be NULL otherwise");
+    if ((r = row_stride(&a.x_row, a.D, "x_row")) != LA_OK || (r = row_stride(&a.g_row, a.D, "g_row")) != LA_OK ||
+        (r = row_stride(&a.h_row, a.D, "h_row")) != LA_OK || (r = row_stride(&a.dh_row, a.D, "dh_row")) != LA_OK ||
+        (r = row_stride(&a.dx_row, a.D, "dx_row")) != LA_OK || (r = row_stride(&a.dg_row, a.D, "dg_row")) != LA_OK)
+        return r;
+    if ((r = elem_aligned({a.x, a.h, a.dh, a.dx}, a.dtype)) != LA_OK ||
+        (r = elem_aligned({a.g, a.dg}, a.gate_dtype)) != LA_OK ||
+        (r = elem_aligned({a.h0, a.dh_last, a.dh0}, LA_F32)) != LA_OK)
+        return r;
+    la::ScanParams p{};
+    p.B = a.B; p.T = a.T; p.D = a.D;
+    p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
+    p.hs = a.h; p.hs_row = a.h_row; p.dh = a.dh; p.dh_row = a.dh_row;
+    p.h0 = a.h0; p.dh_last = a.dh_last;
+    p.dx = a.dx; p.dx_row = a.dx_row; p.dg = a.dg; p.dg_row = a.dg_row; p.dh0 = a.dh0;
+    p.cu_seqlens = a.cu_seqlens; p.max_seqlen = a.max_seqlen;
+    return launch_scan_call<la::ScanOp::kBwd>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+}
+
+la_status la_scan_step(const la_scan_step_args *in, void *stream) {
+    la_scan_step_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    r = validate_scan(a.dtype, a.gate_dtype, a.gate, a.tied, a.N, 1, a.D, nullptr, 0);
+    if (r != LA_OK) return r;
+    if (!a.x || !a.g || !a.state || !a.h) return fail(LA_ERR_INVALID_ARG, "x, g, state and h must be non-NULL");
+    if ((r = row_stride(&a.x_row, a.D, "x_row")) != LA_OK || (r = row_stride(&a.g_row, a.D, "g_row")) != LA_OK ||
+        (r = row_stride(&a.h_row, a.D, "h_row")) != LA_OK)
+        return r;
+    if ((r = elem_aligned({a.x, a.h}, a.dtype)) != LA_OK || (r = elem_aligned({a.g}, a.gate_dtype)) != LA_OK ||
+        (r = elem_aligned({a.state}, LA_F32)) != LA_OK)
+        return r;
+    la::ScanParams p{};
+    p.B = a.N; p.T = 1; p.D = a.D;
+    p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
+    p.h = a.h; p.h_row = a.h_row; p.h_last = a.state;
+    return launch_scan_call<la::ScanOp::kStep>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+}
+
+la_status la_norm_fwd(const la_norm_fwd_args *in, void *stream) {
+    la_norm_fwd_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    if ((r = validate_rows(a.dtype, a.kind, a.R, a.D)) != LA_OK) return r;
+    if (!(a.eps > 0.f) || !std::isfinite(a.eps)) return fail(LA_ERR_INVALID_ARG, "eps must be finite and > 0");
+    if (a.R > 0 && (!a.x || !a.y)) return fail(LA_ERR_INVALID_ARG, "x and y must be non-NULL when R > 0");
+    if (a.kind == LA_NORM_RMS && a.mean) return fail(LA_ERR_INVALID_ARG, "an RMS norm has no mean: it must be NULL");
+    if ((r = row_stride(&a.x_row, a.D, "x_row")) != LA_OK || (r = row_stride(&a.y_row, a.D, "y_row")) != LA_OK) return r;
+    if ((r = elem_aligned({a.x, a.y}, a.dtype)) != LA_OK ||
+        (r = elem_aligned({a.w, a.b, a.mean, a.rstd}, LA_F32)) != LA_OK)
+        return r;
+    if (a.R == 0) return ok();
+    la::NormParams p{};
+    p.R = a.R; p.D = (int)a.D; p.x = a.x; p.x_row = a.x_row; p.w = a.w; p.b = a.b; p.eps = a.eps;
+    p.y = a.y; p.y_row = a.y_row; p.mean = a.mean; p.rstd = a.rstd;
+    const cudaError_t e = la::launch_norm_fwd(p, a.dtype == LA_BF16, a.kind == LA_NORM_LAYER, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(LA_ERR_CUDA, std::string("norm launch: ") + cudaGetErrorString(e));
+    return ok();
+}
+
+la_status la_norm_bwd_workspace_size(const la_norm_bwd_args *in, size_t *bytes) {
+    if (!bytes) return fail(LA_ERR_INVALID_ARG, "bytes is NULL");
+    la_norm_bwd_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    if ((r = validate_rows(a.dtype, a.kind, a.R, a.D)) != LA_OK) return r;
+    *bytes = a.dw || a.db ? la::norm_bwd_workspace(a.R, (int)a.D) : 0;
+    return ok();
+}
+
+la_status la_norm_bwd(const la_norm_bwd_args *in, void *stream) {
+    la_norm_bwd_args a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    if ((r = validate_rows(a.dtype, a.kind, a.R, a.D)) != LA_OK) return r;
+    if (a.R > 0 && (!a.x || !a.dy || !a.dx || !a.rstd))
+        return fail(LA_ERR_INVALID_ARG, "x, dy, rstd and dx must be non-NULL when R > 0");
+    if (a.kind == LA_NORM_RMS ? a.mean != nullptr : a.R > 0 && !a.mean)
+        return fail(LA_ERR_INVALID_ARG, "a layer norm's gradient needs mean; an RMS norm has none (NULL)");
+    if ((r = row_stride(&a.x_row, a.D, "x_row")) != LA_OK || (r = row_stride(&a.dy_row, a.D, "dy_row")) != LA_OK ||
+        (r = row_stride(&a.dx_row, a.D, "dx_row")) != LA_OK)
+        return r;
+    if ((r = elem_aligned({a.x, a.dy, a.dx}, a.dtype)) != LA_OK ||
+        (r = elem_aligned({a.w, a.mean, a.rstd, a.dw, a.db}, LA_F32)) != LA_OK)
+        return r;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a.R == 0) {
+        for (float *o : {a.dw, a.db})
+            if (o) {
+                const cudaError_t e = cudaMemsetAsync(o, 0, (size_t)a.D * sizeof(float), st);
+                if (e != cudaSuccess) return fail(LA_ERR_CUDA, cudaGetErrorString(e));
+            }
+        return ok();
+    }
+    const bool sums = a.dw || a.db;
+    if (sums && (!a.workspace || a.workspace_bytes < la::norm_bwd_workspace(a.R, (int)a.D) || !aligned16(a.workspace)))
+        return fail(LA_ERR_WORKSPACE, "workspace missing, misaligned or smaller than la_norm_bwd_workspace_size()");
+    la::NormParams p{};
+    p.R = a.R; p.D = (int)a.D; p.x = a.x; p.x_row = a.x_row; p.dy = a.dy; p.dy_row = a.dy_row;
+    p.w = a.w; p.mean = const_cast<float *>(a.mean); p.rstd = const_cast<float *>(a.rstd);
+    p.y = a.dx; p.y_row = a.dx_row; p.part = sums ? static_cast<float *>(a.workspace) : nullptr;
+    const cudaError_t e = la::launch_norm_bwd(p, a.dtype == LA_BF16, a.kind == LA_NORM_LAYER, a.dw, a.db, st);
+    if (e != cudaSuccess) return fail(LA_ERR_CUDA, std::string("norm launch: ") + cudaGetErrorString(e));
     return ok();
 }
 

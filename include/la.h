@@ -28,6 +28,10 @@
  *   la_fwd_host  la_fwd on HOST buffers: copies in, runs, copies out.
  *   la_fwd_noalloc  la_fwd with a library-owned scratch array (no allocation).
  *   la_check_device  reads and clears the device-side error word.
+ *   la_scan_fwd, la_scan_bwd, la_scan_step  the gated linear recurrence with a
+ *            vector state (one gate per channel): all outputs and the final state,
+ *            the gradients, one decode token.
+ *   la_norm_fwd, la_norm_bwd  layer norm or RMS norm of rows, and its gradients.
  *
  * Conventions (all entry points)
  *   - Layouts are dense row-major: q,k [B,T,H,dk]; v,o [B,T,H,dv]; GLA gate
@@ -288,6 +292,186 @@ la_status la_fwd_host(const la_fwd_args *host_args, void *staging, size_t stagin
  */
 #define LA_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
 la_status la_fwd_noalloc(const la_fwd_args *args, void *stream);
+
+/*
+ * Gated linear recurrence with a vector state: per sequence and channel
+ *     h_t = a_t h_{t-1} + u_t,   h_{-1} = h0,   every h_t returned, h_last = h_{T-1}
+ * the per-position a, b, x form of a selective scan (page "状态空间与线性注意力",
+ * the selective-scan reference: optional initial state, all outputs and the final
+ * state) with the diagonal transition of gated recurrences.
+ *   gate   LA_GATE_VALUE: a_t = g_t, with |g_t| <= 1 (a larger gate is not
+ *          refused, but a product of gates that overflows fp32 gives infinities or
+ *          NaN);  LA_GATE_LOGIT: a_t = sigmoid(g_t), as a projection gives it.
+ *   tied   0: u_t = x_t;  1: u_t = (1 - a_t) x_t.
+ * The state, the products and every sum are fp32, whatever the types of x and g;
+ * outputs are rounded once.  A NaN or an infinity affects its channel from its
+ * token on, as in the formula.
+ *
+ * Layout (differences from the conventions above are stated here)
+ *   - Token tensors are [B,T,D]; a [B,T,H,d] tensor is D = H d.  The channels of a
+ *     token are contiguous; `*_row` is the distance between consecutive tokens in
+ *     elements (0 means D), so slices of a wider projection are taken as they
+ *     are; consecutive batch entries are T rows apart.  Rows may not overlap.
+ *   - D >= 1 and T >= 0 are not limited otherwise (B D <= 2e9); token pointers
+ *     need the alignment of their element, state pointers that of a float.  Four
+ *     channels per access are used where D, the strides and the pointers are
+ *     multiples of four elements, else one.
+ *   - States h0, h_last, dh_last, dh0 are [B,D] fp32, dense.
+ *   - cu_seqlens / max_seqlen: packed sequences as for la_fwd (token tensors
+ *     [1,T,D], B sequences, each from its own h0[b]); tokens that belong to no
+ *     sequence are neither read nor written.  Bad offsets are clamped and reported
+ *     by la_check_device.
+ *   - No workspace; results do not depend on timing.  T == 0 gives h_last = h0 (or
+ *     zeros) and dh0 = dh_last (or zeros).
+ *   - Outputs must not overlap inputs, except that h_last may be h0 and dh0 may be
+ *     dh_last.
+ */
+typedef enum { LA_GATE_VALUE = 0, LA_GATE_LOGIT = 1 } la_gate;
+
+/* x [B,T,D] of `dtype`, g [B,T,D] of `gate_dtype`; h0 or NULL (zeros);
+ * h [B,T,D] of `dtype` (written); h_last (written) or NULL. */
+typedef struct la_scan_fwd_args {
+    uint32_t struct_size;     /* = sizeof(la_scan_fwd_args) */
+    la_dtype dtype, gate_dtype;
+    la_gate gate;
+    int32_t tied;
+    int64_t B, T, D;
+    const void *x;
+    int64_t x_row;
+    const void *g;
+    int64_t g_row;
+    const float *h0;
+    void *h;
+    int64_t h_row;
+    float *h_last;
+    const int64_t *cu_seqlens;
+    int64_t max_seqlen;
+} la_scan_fwd_args;
+
+/*
+ * Gradients.  With dh the gradient of h, dh_last that of h_last (NULL: zero) and
+ * c_{T-1} = dh_last:
+ *     G_t = dh_t + c_t,  c_{t-1} = a_t G_t,  dh0 = c_{-1},
+ *     dx_t = G_t                    (tied: (1 - a_t) G_t),
+ *     da_t = G_t h_{t-1}            (tied: G_t (h_{t-1} - x_t)),
+ *     dg_t = da_t                   (logit: da_t a_t (1 - a_t)).
+ * h is what la_scan_fwd stored (for bf16 the rounded outputs stand for the state in
+ * da_t).  x is read only when tied (NULL otherwise).  dx [B,T,D] of `dtype` and dg
+ * [B,T,D] of `gate_dtype` are written; dh0 (written) or NULL.
+ */
+typedef struct la_scan_bwd_args {
+    uint32_t struct_size;     /* = sizeof(la_scan_bwd_args) */
+    la_dtype dtype, gate_dtype;
+    la_gate gate;
+    int32_t tied;
+    int64_t B, T, D;
+    const void *x;
+    int64_t x_row;
+    const void *g;
+    int64_t g_row;
+    const void *h;
+    int64_t h_row;
+    const void *dh;
+    int64_t dh_row;
+    const float *h0;
+    const float *dh_last;
+    void *dx;
+    int64_t dx_row;
+    void *dg;
+    int64_t dg_row;
+    float *dh0;
+    const int64_t *cu_seqlens;
+    int64_t max_seqlen;
+} la_scan_bwd_args;
+
+/* One token per sequence: x, g, h [N,D] (row strides as above), state [N,D] fp32
+ * read and overwritten; h is the new state rounded to `dtype`. */
+typedef struct la_scan_step_args {
+    uint32_t struct_size;     /* = sizeof(la_scan_step_args) */
+    la_dtype dtype, gate_dtype;
+    la_gate gate;
+    int32_t tied;
+    int64_t N, D;
+    const void *x;
+    int64_t x_row;
+    const void *g;
+    int64_t g_row;
+    float *state;
+    void *h;
+    int64_t h_row;
+} la_scan_step_args;
+
+/* All asynchronous on `stream`. */
+la_status la_scan_fwd(const la_scan_fwd_args *args, void *stream);
+la_status la_scan_bwd(const la_scan_bwd_args *args, void *stream);
+la_status la_scan_step(const la_scan_step_args *args, void *stream);
+
+/*
+ * Layer norm and RMS norm of R rows of D elements (1 <= D <= LA_NORM_MAX_D):
+ *     LA_NORM_LAYER  xh = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *     LA_NORM_RMS    xh = x rstd,           rstd = 1 / sqrt(mean(x^2) + eps)
+ *     y = xh w + b
+ * The head-wise RMS normalisation of la_fwd's out_norm is LA_NORM_RMS over
+ * R = B T H rows of D = dv.  Gradients, with d = dy w:
+ *     dx = rstd (d - mean(d) - xh mean(d xh))   (RMS: without mean(d)),
+ *     dw = sum over rows of dy xh,  db = sum over rows of dy.
+ * x, y, dy, dx [R,D] of `dtype`, elements of a row contiguous, `*_row` elements
+ * between rows (0 means D), rows not overlapping; w, b, dw, db [D] and mean, rstd
+ * [R] fp32.  w NULL means 1, b NULL means 0.  Statistics and sums are fp32, outputs
+ * are rounded once, and the gradients' sums have a fixed order.  Pointers need the
+ * alignment of their element; 16-byte accesses are used where D, the strides and
+ * the pointers allow them, else single elements.  eps > 0 (finite).
+ * la_norm_fwd writes mean (layer only) and rstd where they are not NULL;
+ * la_norm_bwd reads them (mean: layer only).  dw and db may each be NULL.  R == 0
+ * gives zero dw and db.
+ * Outputs must not overlap inputs.
+ * la_norm_bwd needs la_norm_bwd_workspace_size() bytes of 16-byte aligned device
+ * scratch unless dw and db are both NULL (a row of partial sums for every CTA);
+ * calls that share one must be ordered, as for la_fwd.
+ */
+#define LA_NORM_MAX_D 16384
+typedef enum { LA_NORM_LAYER = 0, LA_NORM_RMS = 1 } la_norm_kind;
+
+typedef struct la_norm_fwd_args {
+    uint32_t struct_size;     /* = sizeof(la_norm_fwd_args) */
+    la_dtype dtype;
+    la_norm_kind kind;
+    int64_t R, D;
+    const void *x;
+    int64_t x_row;
+    const float *w;
+    const float *b;
+    float eps;
+    void *y;
+    int64_t y_row;
+    float *mean;
+    float *rstd;
+} la_norm_fwd_args;
+
+typedef struct la_norm_bwd_args {
+    uint32_t struct_size;     /* = sizeof(la_norm_bwd_args) */
+    la_dtype dtype;
+    la_norm_kind kind;
+    int64_t R, D;
+    const void *x;
+    int64_t x_row;
+    const void *dy;
+    int64_t dy_row;
+    const float *w;
+    const float *mean;
+    const float *rstd;
+    void *dx;
+    int64_t dx_row;
+    float *dw;
+    float *db;
+    void *workspace;
+    size_t workspace_bytes;
+} la_norm_bwd_args;
+
+/* Asynchronous on `stream`; the size query reads R, D, dw and db only. */
+la_status la_norm_fwd(const la_norm_fwd_args *args, void *stream);
+la_status la_norm_bwd(const la_norm_bwd_args *args, void *stream);
+la_status la_norm_bwd_workspace_size(const la_norm_bwd_args *args, size_t *bytes);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word set by
