@@ -31,7 +31,7 @@ STATUS = {0: "LA_OK", 1: "LA_ERR_INVALID_ARG", 2: "LA_ERR_UNSUPPORTED", 3: "LA_E
 EXPORTS = ("la_fwd", "la_fwd_workspace_size", "la_step", "la_fwd_host_staging_size",
            "la_fwd_host", "la_check_device", "la_status_string", "la_last_error_message",
            "la_abi_version", "la_fwd_noalloc", "la_testing_set_wait_limit",
-           "la_scan_fwd", "la_scan_bwd", "la_scan_step",
+           "la_scan_fwd", "la_scan_bwd", "la_scan_step", "la_scan_fwd_workspace_size", "la_scan_bwd_workspace_size",
            "la_norm_fwd", "la_norm_bwd", "la_norm_bwd_workspace_size")
 
 
@@ -70,7 +70,8 @@ _U, _I, _L, _V, _F = ctypes.c_uint32, ctypes.c_int, ctypes.c_int64, ctypes.c_voi
 class ScanFwdArgs(ctypes.Structure):
     _fields_ = [("struct_size", _U), ("dtype", _I), ("gate_dtype", _I), ("gate", _I), ("tied", ctypes.c_int32),
                 ("B", _L), ("T", _L), ("D", _L), ("x", _V), ("x_row", _L), ("g", _V), ("g_row", _L),
-                ("h0", _V), ("h", _V), ("h_row", _L), ("h_last", _V), ("cu_seqlens", _V), ("max_seqlen", _L)]
+                ("h0", _V), ("h", _V), ("h_row", _L), ("h_last", _V), ("cu_seqlens", _V), ("max_seqlen", _L),
+                ("workspace", _V), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class ScanBwdArgs(ctypes.Structure):
@@ -78,7 +79,7 @@ class ScanBwdArgs(ctypes.Structure):
                 ("B", _L), ("T", _L), ("D", _L), ("x", _V), ("x_row", _L), ("g", _V), ("g_row", _L),
                 ("h", _V), ("h_row", _L), ("dh", _V), ("dh_row", _L), ("h0", _V), ("dh_last", _V),
                 ("dx", _V), ("dx_row", _L), ("dg", _V), ("dg_row", _L), ("dh0", _V),
-                ("cu_seqlens", _V), ("max_seqlen", _L)]
+                ("cu_seqlens", _V), ("max_seqlen", _L), ("workspace", _V), ("workspace_bytes", ctypes.c_size_t)]
 
 
 class ScanStepArgs(ctypes.Structure):
@@ -125,10 +126,13 @@ def lib():
         for f, args in ((L.la_scan_fwd, ScanFwdArgs), (L.la_scan_bwd, ScanBwdArgs), (L.la_scan_step, ScanStepArgs),
                         (L.la_norm_fwd, NormFwdArgs), (L.la_norm_bwd, NormBwdArgs)):
             f.argtypes = [ctypes.POINTER(args), P]
-        L.la_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(NormBwdArgs), ctypes.POINTER(ctypes.c_size_t)]
+        for f, args in ((L.la_scan_fwd_workspace_size, ScanFwdArgs), (L.la_scan_bwd_workspace_size, ScanBwdArgs),
+                        (L.la_norm_bwd_workspace_size, NormBwdArgs)):
+            f.argtypes = [ctypes.POINTER(args), ctypes.POINTER(ctypes.c_size_t)]
         for f in (L.la_fwd, L.la_fwd_workspace_size, L.la_step, L.la_fwd_host_staging_size,
                   L.la_fwd_host, L.la_check_device, L.la_fwd_noalloc, L.la_scan_fwd, L.la_scan_bwd,
-                  L.la_scan_step, L.la_norm_fwd, L.la_norm_bwd, L.la_norm_bwd_workspace_size):
+                  L.la_scan_step, L.la_scan_fwd_workspace_size, L.la_scan_bwd_workspace_size,
+                  L.la_norm_fwd, L.la_norm_bwd, L.la_norm_bwd_workspace_size):
             f.restype = ctypes.c_int
         L.la_abi_version.restype = ctypes.c_int
         if L.la_abi_version() != ABI_VERSION:
@@ -404,6 +408,18 @@ class _On:
         return False
 
 
+def _workspace(size_of, a, device):
+    """The scratch that ``size_of`` asks for, allocated for this call and set in ``a``
+    (calls on different streams and captured graphs share none)."""
+    n = ctypes.c_size_t()
+    _check(size_of(ctypes.byref(a), ctypes.byref(n)))
+    if not n.value:
+        return None
+    ws = torch.empty(n.value, dtype=torch.uint8, device=device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), n.value
+    return ws
+
+
 def _choice(table, key, name):
     try:
         return table[key]
@@ -457,6 +473,7 @@ def scan_fwd(x, g, h0=None, gate: str = "value", tied: bool = False, h=None, h_l
         a = ScanFwdArgs(ctypes.sizeof(ScanFwdArgs), dt, gd, gt, 1 if tied else 0, N, lead[1], D,
                         x.data_ptr(), xr, g.data_ptr(), gr, _dense(h0, "h0", state, dev), h.data_ptr(),
                         _tokens(h, "h", lead, tail, x.dtype, dev), _dense(h_last, "h_last", state, dev), cu, ms)
+        ws = _workspace(lib().la_scan_fwd_workspace_size, a, dev)  # noqa: F841 (kept until the call is queued)
         _check(lib().la_scan_fwd(ctypes.byref(a), st))
     return h, h_last
 
@@ -491,6 +508,7 @@ def scan_bwd(g, h, dh, x=None, h0=None, dh_last=None, gate: str = "value", tied:
                         dx.data_ptr(), _tokens(dx, "dx", lead, tail, dh.dtype, dev),
                         dg.data_ptr(), _tokens(dg, "dg", lead, tail, g.dtype, dev),
                         _dense(dh0, "dh0", state, dev), cu, ms)
+        ws = _workspace(lib().la_scan_bwd_workspace_size, a, dev)  # noqa: F841
         _check(lib().la_scan_bwd(ctypes.byref(a), st))
     return dx, dg, dh0
 
@@ -573,11 +591,7 @@ def norm_bwd(dy, x, rstd, mean=None, w=None, kind: str = "layer", dx=None, want_
                         _tokens(dx, "dx", lead, tail, x.dtype, dev),
                         dw.data_ptr() if want_dw else None, db.data_ptr() if want_db else None, None, 0)
         if want_dw or want_db:
-            n = ctypes.c_size_t()
-            _check(lib().la_norm_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)))
-            if n.value:
-                ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-                a.workspace, a.workspace_bytes = ws.data_ptr(), n.value
+            ws = _workspace(lib().la_norm_bwd_workspace_size, a, dev)  # noqa: F841
         _check(lib().la_norm_bwd(ctypes.byref(a), st))
     return dx, dw, db
 

@@ -158,6 +158,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }  // namespace
 
 namespace la {
+// 2-D map over `tokens` rows of D elements (fp32 or bf16) that lie `row` elements
+// apart, box {box_d, box_t}; what lies outside reads as zero and is not written.
+bool make_map_2d(CUtensorMap *map, const void *base, int esize, int64_t D, int64_t tokens, int64_t row, int box_d, int box_t) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)(row * esize)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_d, (cuuint32_t)box_t}, es[2] = {1, 1};
+    return fn(map, esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4-D map over a [B,T,H,D] tensor (innermost first: D, H, T, B), box
 // {box_d, 1, box_t, 1}.  Rows past T read as zero.
 bool make_map_4d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, int esize,
@@ -605,6 +617,7 @@ la_status validate_scan(la_dtype dtype, la_dtype gate_dtype, la_gate gate, int32
         return fail(LA_ERR_INVALID_ARG, "gate must be LA_GATE_VALUE or LA_GATE_LOGIT");
     if (tied != 0 && tied != 1) return fail(LA_ERR_INVALID_ARG, "tied must be 0 or 1");
     if (B < 1 || T < 0 || D < 1) return fail(LA_ERR_INVALID_ARG, "need at least one sequence, T >= 0 and D >= 1");
+    if (T > (1 << 30)) return fail(LA_ERR_UNSUPPORTED, "sequences of more than 2^30 tokens have no kernel");
     if ((double)B * (double)D > 2.0e9 || (double)B * (double)(T > 0 ? T : 1) * (double)D > 1.0e18)
         return fail(LA_ERR_INVALID_ARG, "problem too large");
     if (cu) {
@@ -622,14 +635,40 @@ la_status elem_aligned(std::initializer_list<const void *> ps, la_dtype t) {
     return LA_OK;
 }
 
+// The scratch of a scan over these sequences, checked against the caller's if `check`.
+template <typename A>
+la_status scan_workspace(const A &a, la::ScanParams &p, size_t *bytes, bool check) {
+    constexpr bool kBwd = std::is_same_v<A, la_scan_bwd_args>;
+    p.B = a.B; p.T = a.T; p.D = a.D;
+    p.cu_seqlens = a.cu_seqlens; p.max_seqlen = a.max_seqlen;
+    *bytes = la::scan_scratch(p, la::scan_elem((int)elem_size(a.dtype), (int)elem_size(a.gate_dtype), kBwd, a.tied != 0));
+    if (!check || *bytes == 0) return LA_OK;
+    if (!a.workspace || a.workspace_bytes < *bytes || !aligned16(a.workspace))
+        return fail(LA_ERR_WORKSPACE, "workspace missing, misaligned or smaller than la_scan_*_workspace_size()");
+    p.scratch = a.workspace;
+    return LA_OK;
+}
+template <typename A>
+la_status scan_workspace_size(const A *in, size_t *bytes) {
+    if (!bytes) return fail(LA_ERR_INVALID_ARG, "bytes is NULL");
+    A a;
+    la_status r = load_args(in, &a);
+    if (r != LA_OK) return r;
+    r = validate_scan(a.dtype, a.gate_dtype, a.gate, a.tied, a.B, a.T, a.D, a.cu_seqlens, a.max_seqlen);
+    if (r != LA_OK) return r;
+    la::ScanParams p{};
+    r = scan_workspace(a, p, bytes, false);
+    return r == LA_OK ? ok() : r;
+}
+
 template <la::ScanOp OP>
-la_status launch_scan_call(const la::ScanParams &p, la_dtype dt, la_dtype gt, bool logit, bool tied, void *stream) {
+la_status launch_scan_call(const la::ScanParams &p, la_dtype dt, la_dtype gt, void *stream) {
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     using bf = __nv_bfloat16;
-    const cudaError_t e = dt == LA_BF16 ? (gt == LA_BF16 ? la::launch_scan<OP, bf, bf>(p, logit, tied, st)
-                                                         : la::launch_scan<OP, bf, float>(p, logit, tied, st))
-                                        : (gt == LA_BF16 ? la::launch_scan<OP, float, bf>(p, logit, tied, st)
-                                                         : la::launch_scan<OP, float, float>(p, logit, tied, st));
+    const cudaError_t e = dt == LA_BF16 ? (gt == LA_BF16 ? la::launch_scan<OP, bf, bf>(p, st)
+                                                         : la::launch_scan<OP, bf, float>(p, st))
+                                        : (gt == LA_BF16 ? la::launch_scan<OP, float, bf>(p, st)
+                                                         : la::launch_scan<OP, float, float>(p, st));
     if (e != cudaSuccess) return fail(LA_ERR_CUDA, std::string("scan launch: ") + cudaGetErrorString(e));
     return ok();
 }
@@ -662,12 +701,16 @@ la_status la_scan_fwd(const la_scan_fwd_args *in, void *stream) {
         (r = elem_aligned({a.h0, a.h_last}, LA_F32)) != LA_OK)
         return r;
     la::ScanParams p{};
-    p.B = a.B; p.T = a.T; p.D = a.D;
+    size_t need = 0;
+    if ((r = scan_workspace(a, p, &need, true)) != LA_OK) return r;
+    p.logit = a.gate == LA_GATE_LOGIT; p.tied = a.tied;
     p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
     p.h0 = a.h0; p.h = a.h; p.h_row = a.h_row; p.h_last = a.h_last;
-    p.cu_seqlens = a.cu_seqlens; p.max_seqlen = a.max_seqlen;
-    return launch_scan_call<la::ScanOp::kFwd>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+    return launch_scan_call<la::ScanOp::kFwd>(p, a.dtype, a.gate_dtype, stream);
 }
+
+la_status la_scan_fwd_workspace_size(const la_scan_fwd_args *in, size_t *bytes) { return scan_workspace_size(in, bytes); }
+la_status la_scan_bwd_workspace_size(const la_scan_bwd_args *in, size_t *bytes) { return scan_workspace_size(in, bytes); }
 
 la_status la_scan_bwd(const la_scan_bwd_args *in, void *stream) {
     la_scan_bwd_args a;
@@ -688,13 +731,14 @@ la_status la_scan_bwd(const la_scan_bwd_args *in, void *stream) {
         (r = elem_aligned({a.h0, a.dh_last, a.dh0}, LA_F32)) != LA_OK)
         return r;
     la::ScanParams p{};
-    p.B = a.B; p.T = a.T; p.D = a.D;
+    size_t need = 0;
+    if ((r = scan_workspace(a, p, &need, true)) != LA_OK) return r;
+    p.logit = a.gate == LA_GATE_LOGIT; p.tied = a.tied;
     p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
     p.hs = a.h; p.hs_row = a.h_row; p.dh = a.dh; p.dh_row = a.dh_row;
     p.h0 = a.h0; p.dh_last = a.dh_last;
     p.dx = a.dx; p.dx_row = a.dx_row; p.dg = a.dg; p.dg_row = a.dg_row; p.dh0 = a.dh0;
-    p.cu_seqlens = a.cu_seqlens; p.max_seqlen = a.max_seqlen;
-    return launch_scan_call<la::ScanOp::kBwd>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+    return launch_scan_call<la::ScanOp::kBwd>(p, a.dtype, a.gate_dtype, stream);
 }
 
 la_status la_scan_step(const la_scan_step_args *in, void *stream) {
@@ -712,9 +756,10 @@ la_status la_scan_step(const la_scan_step_args *in, void *stream) {
         return r;
     la::ScanParams p{};
     p.B = a.N; p.T = 1; p.D = a.D;
+    p.logit = a.gate == LA_GATE_LOGIT; p.tied = a.tied;
     p.x = a.x; p.x_row = a.x_row; p.g = a.g; p.g_row = a.g_row;
     p.h = a.h; p.h_row = a.h_row; p.h_last = a.state;
-    return launch_scan_call<la::ScanOp::kStep>(p, a.dtype, a.gate_dtype, a.gate == LA_GATE_LOGIT, a.tied != 0, stream);
+    return launch_scan_call<la::ScanOp::kStep>(p, a.dtype, a.gate_dtype, stream);
 }
 
 la_status la_norm_fwd(const la_norm_fwd_args *in, void *stream) {

@@ -312,17 +312,20 @@ la_status la_fwd_noalloc(const la_fwd_args *args, void *stream);
  *     token are contiguous; `*_row` is the distance between consecutive tokens in
  *     elements (0 means D), so slices of a wider projection are taken as they
  *     are; consecutive batch entries are T rows apart.  Rows may not overlap.
- *   - D >= 1 and T >= 0 are not limited otherwise (B D <= 2e9); token pointers
- *     need the alignment of their element, state pointers that of a float.  Four
- *     channels per access are used where D, the strides and the pointers are
- *     multiples of four elements, else one.
+ *   - D >= 1, 0 <= T <= 2^30 and B D <= 2e9; token pointers
+ *     need the alignment of their element, state pointers that of a float.  Tokens
+ *     are moved as tiles where every row's address is a multiple of 16 bytes (one
+ *     token: of four elements), else element by element.
  *   - States h0, h_last, dh_last, dh0 are [B,D] fp32, dense.
  *   - cu_seqlens / max_seqlen: packed sequences as for la_fwd (token tensors
  *     [1,T,D], B sequences, each from its own h0[b]); tokens that belong to no
  *     sequence are neither read nor written.  Bad offsets are clamped and reported
  *     by la_check_device.
- *   - No workspace; results do not depend on timing.  T == 0 gives h_last = h0 (or
- *     zeros) and dh0 = dh_last (or zeros).
+ *   - la_scan_fwd and la_scan_bwd need the bytes that la_scan_*_workspace_size() gives
+ *     of 16-byte aligned device scratch (0 for short sequences: none is needed).  Its
+ *     contents before a call do not matter; calls that share one must be ordered, as
+ *     for la_fwd.  Results do not depend on timing.
+ *   - T == 0 gives h_last = h0 (or zeros) and dh0 = dh_last (or zeros).
  *   - Outputs must not overlap inputs, except that h_last may be h0 and dh0 may be
  *     dh_last.
  */
@@ -346,6 +349,8 @@ typedef struct la_scan_fwd_args {
     float *h_last;
     const int64_t *cu_seqlens;
     int64_t max_seqlen;
+    void *workspace;
+    size_t workspace_bytes;
 } la_scan_fwd_args;
 
 /*
@@ -382,6 +387,8 @@ typedef struct la_scan_bwd_args {
     float *dh0;
     const int64_t *cu_seqlens;
     int64_t max_seqlen;
+    void *workspace;
+    size_t workspace_bytes;
 } la_scan_bwd_args;
 
 /* One token per sequence: x, g, h [N,D] (row strides as above), state [N,D] fp32
@@ -405,6 +412,10 @@ typedef struct la_scan_step_args {
 la_status la_scan_fwd(const la_scan_fwd_args *args, void *stream);
 la_status la_scan_bwd(const la_scan_bwd_args *args, void *stream);
 la_status la_scan_step(const la_scan_step_args *args, void *stream);
+
+/* Scratch of a call; reads the types, tied, B, T, D and whether cu_seqlens is NULL. */
+la_status la_scan_fwd_workspace_size(const la_scan_fwd_args *args, size_t *bytes);
+la_status la_scan_bwd_workspace_size(const la_scan_bwd_args *args, size_t *bytes);
 
 /*
  * Layer norm and RMS norm of R rows of D elements (1 <= D <= LA_NORM_MAX_D):
