@@ -56,6 +56,16 @@ struct RowVec<__nv_bfloat16, 4> {
     __device__ __forceinline__ void zero() { r = make_uint2(0u, 0u); }
 };
 template <>
+struct RowVec<__nv_bfloat16, 2> {
+    uint32_t r;
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? (r & 0xffff0000u) : (r << 16)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = __ldg(reinterpret_cast<const uint32_t *>(p)); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
+        *reinterpret_cast<uint32_t *>(p) = pack_bf16x2(v[0], v[1]);
+    }
+    __device__ __forceinline__ void zero() { r = 0u; }
+};
+template <>
 struct RowVec<__nv_bfloat16, 1> {
     unsigned short r;
     __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)r << 16); }
