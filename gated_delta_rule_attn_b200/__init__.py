@@ -388,15 +388,16 @@ class _On:
             if stream.device != device:
                 raise ValueError("stream belongs to another device than the tensors")
             self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
+        elif torch._C._cuda_getDevice() != device.index:
             self.ctx = torch.cuda.device(device)
         self.device, self.stream, self.tensors = device, stream, tensors
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.stream is not None:
@@ -408,7 +409,7 @@ class _On:
         return False
 
 
-def _workspace(size_of, a, device):
+def _call_scratch(size_of, a, device):
     """The scratch that ``size_of`` asks for, allocated for this call and set in ``a``
     (calls on different streams and captured graphs share none)."""
     n = ctypes.c_size_t()
@@ -473,7 +474,7 @@ def scan_fwd(x, g, h0=None, gate: str = "value", tied: bool = False, h=None, h_l
         a = ScanFwdArgs(ctypes.sizeof(ScanFwdArgs), dt, gd, gt, 1 if tied else 0, N, lead[1], D,
                         x.data_ptr(), xr, g.data_ptr(), gr, _dense(h0, "h0", state, dev), h.data_ptr(),
                         _tokens(h, "h", lead, tail, x.dtype, dev), _dense(h_last, "h_last", state, dev), cu, ms)
-        ws = _workspace(lib().la_scan_fwd_workspace_size, a, dev)  # noqa: F841 (kept until the call is queued)
+        ws = _call_scratch(lib().la_scan_fwd_workspace_size, a, dev)  # noqa: F841 (kept until the call is queued)
         _check(lib().la_scan_fwd(ctypes.byref(a), st))
     return h, h_last
 
@@ -508,7 +509,7 @@ def scan_bwd(g, h, dh, x=None, h0=None, dh_last=None, gate: str = "value", tied:
                         dx.data_ptr(), _tokens(dx, "dx", lead, tail, dh.dtype, dev),
                         dg.data_ptr(), _tokens(dg, "dg", lead, tail, g.dtype, dev),
                         _dense(dh0, "dh0", state, dev), cu, ms)
-        ws = _workspace(lib().la_scan_bwd_workspace_size, a, dev)  # noqa: F841
+        ws = _call_scratch(lib().la_scan_bwd_workspace_size, a, dev)  # noqa: F841
         _check(lib().la_scan_bwd(ctypes.byref(a), st))
     return dx, dg, dh0
 
@@ -555,9 +556,10 @@ def norm_fwd(x, w=None, b=None, kind: str = "layer", eps: float = 1e-6, y=None, 
             y = torch.empty(x.shape, dtype=x.dtype, device=dev)
         mean = rstd = None
         if want_stats:
-            rstd = torch.empty(lead, dtype=torch.float32, device=dev)
             if kd == 0:
-                mean = torch.empty(lead, dtype=torch.float32, device=dev)
+                mean, rstd = torch.empty((2,) + lead, dtype=torch.float32, device=dev).unbind(0)
+            else:
+                rstd = torch.empty(lead, dtype=torch.float32, device=dev)
         a = NormFwdArgs(ctypes.sizeof(NormFwdArgs), dt, kd, lead.numel(), tail[0], x.data_ptr(), xr,
                         _dense(w, "w", tail, dev), _dense(b, "b", tail, dev), eps, y.data_ptr(),
                         _tokens(y, "y", lead, tail, x.dtype, dev),
@@ -591,7 +593,7 @@ def norm_bwd(dy, x, rstd, mean=None, w=None, kind: str = "layer", dx=None, want_
                         _tokens(dx, "dx", lead, tail, x.dtype, dev),
                         dw.data_ptr() if want_dw else None, db.data_ptr() if want_db else None, None, 0)
         if want_dw or want_db:
-            ws = _workspace(lib().la_norm_bwd_workspace_size, a, dev)  # noqa: F841
+            ws = _call_scratch(lib().la_norm_bwd_workspace_size, a, dev)  # noqa: F841
         _check(lib().la_norm_bwd(ctypes.byref(a), st))
     return dx, dw, db
 

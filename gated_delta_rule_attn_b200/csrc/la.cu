@@ -18,7 +18,9 @@
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
+#include <map>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "la.h"
@@ -193,11 +195,26 @@ bool make_map_4d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, 
 // Opt the kernel in to `bytes` of dynamic shared memory and ask for the largest
 // shared-memory carveout, so that several CTAs of a small-footprint kernel can
 // be resident on one SM (and the occupancy query counts them).
+// Asked of the runtime once per kernel, device and size: the two calls take longer than
+// a launch of few rows.
 cudaError_t allow_smem(const void *kernel, int bytes) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 (int)cudaSharedmemCarveoutMaxShared);
+    static std::mutex lock;
+    static std::map<std::pair<const void *, int>, int> allowed;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    try {
+        std::lock_guard<std::mutex> hold(lock);
+        const auto at = allowed.find({kernel, dev});
+        if (at != allowed.end() && at->second >= bytes) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     (int)cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess) allowed[{kernel, dev}] = bytes;
+    } catch (const std::bad_alloc &) {
+        e = cudaErrorMemoryAllocation;
+    }
     return e;
 }
 }  // namespace la
