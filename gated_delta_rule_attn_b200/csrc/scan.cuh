@@ -488,11 +488,14 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
             }
         }
     };
+    // (a 1 that the compiler does not know, so that every gate passes through a product)
+    float one;
+    asm volatile("mov.f32 %0, 0f3F800000;" : "=f"(one));
     const float2 zero = make_float2(0.f, 0.f), reset = make_float2(__uint_as_float(kScanReset), __uint_as_float(kScanReset));
 
     if constexpr (MAP) {
         const float2 s = start >= 0 ? state(s_in, start) : zero;
-        ScanMap m{make_float2(1.f, 1.f), s};
+        ScanMap m{make_float2(one, one), s};
         for (int k = 0; k < count; ++k) {
             arrived(slot);
             const int t = origin + k * R;
@@ -508,27 +511,27 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
     } else {
         if (!TEAM && P.S > 1) asm volatile("griddepcontrol.wait;" ::: "memory");   // the segments' maps
         // sequences without tokens pass their state on; bad offsets are reported
-        if (seg == 0 && rank == 0 && (!TEAM || warp == 0))
-            for (int i = 0; i < seqs.n; i += 32) {
-                const int j = i + lane;
-                const bool in = j < seqs.n;
-                uint32_t none = __ballot_sync(0xffffffffu, in && seqs.bound(j + 1) <= seqs.bound(j));
-                for (; none; none &= none - 1) {
-                    const int e = i + __ffs(none) - 1;
-                    put_state(s_out, e, state(s_in, e));
-                }
-                if (seqs.cu && c0 == 0 && in) {
-                    const int64_t s = seqs.cu[j], e = seqs.cu[j + 1];
-                    if (s < 0 || e < s || e > P.T || e - s > P.max_seqlen) raise_error(kErrSeqlen);
-                }
+        const int worker = TEAM ? rank * W + warp : seg, workers = TEAM ? K * W : P.S;
+        for (int i = worker * 32; i < seqs.n; i += workers * 32) {
+            const int j = i + lane;
+            const bool in = j < seqs.n;
+            uint32_t none = __ballot_sync(0xffffffffu, in && seqs.bound(j + 1) <= seqs.bound(j));
+            for (; none; none &= none - 1) {
+                const int e = i + __ffs(none) - 1;
+                put_state(s_out, e, state(s_in, e));
             }
+            if (seqs.cu && c0 == 0 && in) {
+                const int64_t s = seqs.cu[j], e = seqs.cu[j + 1];
+                if (s < 0 || e < s || e > P.T || e - s > P.max_seqlen) raise_error(kErrSeqlen);
+            }
+        }
         if (count <= 0) return;
         // The state that enters the segment, or a team's round.  The walk's first place is the start
         // of a sequence, so the first map forgets what is before it.
         float2 h = zero, carry = zero, last = zero;
         const bool cut = !TEAM && seg + 1 < P.S;
         if (!TEAM) {
-#pragma unroll 4
+#pragma unroll 16
             for (int i = 0; i < seg; ++i) map_apply(map_load(maps + (size_t)i * P.nblk * 32), h);
             if (cut) last = begins[(size_t)seg * P.nblk * 32];
         }
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
             if constexpr (TEAM) {
                 kept_start = starts ? seqs.walk_to(at - 1, t + 31 - __clz(starts)) : -1;
                 if (starts) last = state(s_in, kept_start);
-                ScanMap m{make_float2(1.f, 1.f), zero};
+                ScanMap m{make_float2(one, one), zero};
                 if (n > 0) {
                     arrived(slot);
                     compose(m, slot, 0, n, starts, [&](int r) { return begin(seqs.walk_to(at - 1, t + r)); });
@@ -716,6 +719,7 @@ cudaError_t allow_smem(const void *kernel, int bytes);   // la.cu
 constexpr int kScanShort = 512;     // tokens: below, one warp takes the walk
 constexpr int kScanMany = 296;      // channel blocks: from there on too
 constexpr int kScanFew = 64;        // channel blocks: below, two kernels
+constexpr int64_t kScanMaxS = 512;  // segments: their maps are applied one after the other
 struct ScanPlan {
     int n;                          // sequences per walk
     int64_t nblk, S, L;             // S > 1: two kernels
@@ -741,7 +745,7 @@ inline ScanPlan scan_plan(const ScanParams &p, int elem, bool vec) {
             q.W = elem <= 6 ? 2 * kScanW : kScanW;
             q.NS = 2;
         } else {
-            S = std::max<int64_t>(1, std::min(warps / q.nblk, len / (4 * kScanR)));
+            S = std::max<int64_t>(1, std::min<int64_t>({warps / q.nblk, len / (4 * kScanR), kScanMaxS}));
         }
     } else if (vec) {
         // few warps: as many slots as the SM's share has room for
@@ -844,7 +848,8 @@ cudaError_t launch_step(ScanParams p, cudaStream_t st) {
 enum class ScanOp { kFwd, kBwd, kStep };
 
 // TMA takes rows whose address and distance are multiples of 16 bytes (the distance
-// below 2^40), on a token axis of less than 2^31 tokens.
+// below 2^40), on a token axis of less than 2^31 tokens.  The rows' lengths have to be
+// multiples of 16 bytes too: a store's end is cut at those only.
 inline bool scan_tma_ok(const void *p, int64_t row, int esize) {
     return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && row * esize % 16 == 0 && row * esize < (1ll << 40));
 }
@@ -869,7 +874,8 @@ cudaError_t launch_scan(const ScanParams &p, cudaStream_t st) {
         }
     } else {
         constexpr bool B = OP == ScanOp::kBwd;
-        const bool vec = (p.cu_seqlens ? 1 : p.B) * p.T < (1ll << 31) - 1 && scan_tma_ok(p.x, p.x_row, ex) &&
+        const bool vec = (p.cu_seqlens ? 1 : p.B) * p.T < (1ll << 31) - 1 && p.D * ex % 16 == 0 && p.D * eg % 16 == 0 &&
+                         scan_tma_ok(p.x, p.x_row, ex) &&
                          scan_tma_ok(p.g, p.g_row, eg) && scan_tma_ok(p.h, p.h_row, ex) &&
                          scan_tma_ok(p.hs, p.hs_row, ex) && scan_tma_ok(p.dh, p.dh_row, ex) &&
                          scan_tma_ok(p.dx, p.dx_row, ex) && scan_tma_ok(p.dg, p.dg_row, eg);

@@ -314,8 +314,8 @@ la_status la_fwd_noalloc(const la_fwd_args *args, void *stream);
  *     are; consecutive batch entries are T rows apart.  Rows may not overlap.
  *   - D >= 1, 0 <= T <= 2^30 and B D <= 2e9; token pointers
  *     need the alignment of their element, state pointers that of a float.  Tokens
- *     are moved as tiles where every row's address is a multiple of 16 bytes (one
- *     token: of four elements), else element by element.
+ *     are moved as tiles where every row's address and length are multiples of 16
+ *     bytes (one token: of four elements), else element by element.
  *   - States h0, h_last, dh_last, dh0 are [B,D] fp32, dense.
  *   - cu_seqlens / max_seqlen: packed sequences as for la_fwd (token tensors
  *     [1,T,D], B sequences, each from its own h0[b]); tokens that belong to no

@@ -472,3 +472,175 @@ def test_scan_refuses(la):
         la.scan_step(x[:, 0], g[:, 0], None)
     with pytest.raises(ValueError):
         la.scan_fwd(x[:1], g[:1], cu_seqlens=torch.tensor([0, 8], dtype=torch.int32, device="cuda"), max_seqlen=8)
+
+
+# The three ways of dividing a walk (whole walks, teams, maps and then outputs) at the
+# channel counts that choose them, with sequences that start and end anywhere.
+@pytest.mark.parametrize("D", [4096, 4104, 8192, 19008, 20])
+@pytest.mark.parametrize("gate,tied", [("value", False), ("logit", True)])
+def test_scan_packed_many_channels(la, D, gate, tied):
+    lens = [1, 0, 15, 16, 17, 300, 2, 1, 1, 0, 129, 128, 640]
+    n, total = len(lens), sum(lens)
+    p = make(31 + D, 1, total, D, BF, BF if gate == "logit" else F32, gate)
+    st = make(32 + D, n, 1, D)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int64)
+    kw = dict(gate=gate, tied=tied, cu_seqlens=cu.cuda(), max_seqlen=max(lens))
+    s = c(st["h0"])
+    h, last = la.scan_fwd(c(p["x"]), c(p["g"]), s, h_last=s, **kw)       # the state in place
+    e = c(st["dl"])
+    dx, dg, dh0 = la.scan_bwd(c(p["g"]), h, c(p["dh"]), x=c(p["x"]) if tied else None, h0=c(st["h0"]), dh_last=e,
+                              dh0=e, **kw)
+    la.check_device()
+    pick = torch.randperm(D, generator=torch.Generator().manual_seed(D))[:24]     # the oracle's channels
+    for i in range(n):
+        sl = slice(int(cu[i]), int(cu[i + 1]))
+        one = lambda t: t[:, sl][..., pick.to(t.device)]  # noqa: E731
+        h0, dl = st["h0"][i:i + 1][:, pick], st["dl"][i:i + 1][:, pick]
+        check_fwd(one(h), last[i:i + 1][:, pick.cuda()], one(p["x"]), one(p["g"]), h0, gate, tied, (i, lens[i]))
+        check_bwd((one(dx), one(dg), dh0[i:i + 1][:, pick.cuda()]), one(p["g"]), one(h), one(p["dh"]), one(p["x"]), h0,
+                  dl, gate, tied, (i, lens[i]))
+
+
+def test_scan_thousands_of_sequences(la):
+    """More sequences than one search step sees, most of them short, some empty."""
+    gen = torch.Generator().manual_seed(33)
+    lens = torch.randint(0, 6, (3000,), generator=gen)
+    lens[1500] = 700
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    total, D = int(cu[-1]), 12
+    p, st = make(34, 1, total, D), make(35, 3000, 1, D)
+    h, last = la.scan_fwd(c(p["x"]), c(p["g"]), c(st["h0"]), cu_seqlens=cu.cuda(), max_seqlen=700)
+    got = la.scan_bwd(c(p["g"]), h, c(p["dh"]), h0=c(st["h0"]), dh_last=c(st["dl"]), cu_seqlens=cu.cuda(), max_seqlen=700)
+    la.check_device()
+    for i in [0, 1, 2, 31, 32, 33, 1023, 1024, 1499, 1500, 1501, 2998, 2999] + list(range(700, 760)):
+        s = slice(int(cu[i]), int(cu[i + 1]))
+        check_fwd(h[:, s], last[i:i + 1], p["x"][:, s], p["g"][:, s], st["h0"][i:i + 1], "value", False, i)
+        check_bwd((got[0][:, s], got[1][:, s], got[2][i:i + 1]), p["g"][:, s], h[:, s], p["dh"][:, s], None,
+                  st["h0"][i:i + 1], st["dl"][i:i + 1], "value", False, i)
+
+
+@pytest.mark.parametrize("B,T,D", [(300, 1, 40), (500, 7, 64), (130, 63, 72), (90, 64, 8), (2000, 3, 5)])
+def test_scan_short_dense_sequences(la, B, T, D):
+    """Short dense sequences are walked as one axis."""
+    run_both(la, make(36 + B, B, T, D), "value", True)
+    run_both(la, make(37 + B, B, T, D, BF, BF, "logit"), "logit", False, state=False)
+
+
+def test_scan_odd_channels_in_aligned_rows(la):
+    """A channel count that is no multiple of a tile in rows that are multiples of 16 bytes."""
+    p = make(38, 1, 900, 1001, BF, F32)
+    wide = lambda t, w: torch.full((1, 900, w), 7.0, dtype=t.dtype, device="cuda")  # noqa: E731
+    x, g, out, dx, dg = wide(p["x"], 1008), wide(p["g"], 1004), wide(p["x"], 1016), wide(p["x"], 1008), wide(p["g"], 1004)
+    x[..., :1001] = c(p["x"])
+    g[..., :1001] = c(p["g"])
+    h, last = la.scan_fwd(x[..., :1001], g[..., :1001], c(p["h0"]), h=out[..., :1001])
+    check_fwd(h, last, p["x"], p["g"], p["h0"], "value", False)
+    got = la.scan_bwd(g[..., :1001], h, c(p["dh"]), h0=c(p["h0"]), dh_last=c(p["dl"]), dx=dx[..., :1001], dg=dg[..., :1001])
+    check_bwd(got, p["g"], h, p["dh"], None, p["h0"], p["dl"], "value", False)
+    for t in (out, dx, dg):
+        assert torch.all(t[..., 1001:] == 7.0)
+
+
+@pytest.mark.parametrize("D,T", [(4096, 700), (8, 700), (20000, 40), (8, 3)])
+def test_scan_infinity_stays_in_its_sequence(la, D, T):
+    """What a sequence left, infinities and NaN included, does not reach the next one; a
+    NaN gate of any bits makes its channel NaN to the end of its sequence."""
+    cut = T // 2
+    cu = torch.tensor([0, cut, T], dtype=torch.int64, device="cuda")
+    p = make(39, 1, T, D)
+    x, g = c(p["x"]), c(p["g"])
+    clean, cl = la.scan_fwd(x, g, cu_seqlens=cu, max_seqlen=T)
+    y = x.clone()
+    y[0, 0, 1], y[0, cut - 1, 2] = float("inf"), float("nan")
+    gg = g.clone()
+    gg.view(torch.int32)[0, 0, 3] = 0x7FA5C31D
+    h, last = la.scan_fwd(y, gg, cu_seqlens=cu, max_seqlen=T)
+    assert torch.equal(h[0, cut:], clean[0, cut:]) and torch.equal(last[1], cl[1])
+    assert torch.isnan(h[0, :cut, 3]).all() and torch.isnan(last[0, 3]) and torch.isinf(h[0, 0, 1])
+    dh = x.clone()
+    dh[0, T - 1, 1], dh[0, cut, 2] = float("inf"), float("nan")
+    a = la.scan_bwd(g, clean, x, cu_seqlens=cu, max_seqlen=T)
+    b = la.scan_bwd(g, clean, dh, cu_seqlens=cu, max_seqlen=T)
+    assert torch.equal(a[0][0, :cut], b[0][0, :cut]) and torch.equal(a[2][0], b[2][0]) and torch.isnan(b[2][1, 2])
+
+
+@pytest.mark.parametrize("D", [4096, 16])
+def test_scan_two_at_once(la, D):
+    """Two calls on two streams, whose CTAs share the SMs: each has scratch of its own."""
+    ps = [make(40 + i, 1, 4000, D, BF, BF, "logit") for i in range(2)]
+    dev = [{k: c(v) for k, v in p.items()} for p in ps]
+    want = [la.scan_fwd(d["x"], d["g"], d["h0"], gate="logit", tied=True) for d in dev]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(la.scan_fwd(dev[i]["x"], dev[i]["g"], dev[i]["h0"], gate="logit", tied=True, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for h, last in got[i]:
+            assert torch.equal(h, want[i][0]) and torch.equal(last, want[i][1])
+
+
+def test_scan_short_wait_limit_reports_timeout(la):
+    """Waits that run out are reported; the boxes and a team's messages are still waited
+    for, so the next call on the same context is right."""
+    p = make(42, 1, 5000, 4096)
+    x, g = c(p["x"]), c(p["g"])
+    want, wl = la.scan_fwd(x, g)
+    la.check_device()
+    prev = ctypes.c_int64(0)
+    L = la.lib()
+    assert L.la_testing_set_wait_limit(1, ctypes.byref(prev)) == 0
+    try:
+        la.scan_fwd(x, g)
+        with pytest.raises(la.LAError) as e:
+            la.check_device()
+        assert e.value.status == 5
+    finally:
+        assert L.la_testing_set_wait_limit(prev.value, None) == 0
+    h, last = la.scan_fwd(x, g)
+    la.check_device()
+    assert torch.equal(h, want) and torch.equal(last, wl)
+
+
+def test_recurrent_block_trains_and_serves(la):
+    """Norm, gates, recurrence and norm as a block uses them: one step of gradients through
+    the kernels' own backward passes against fp64 autograd, then tokens one at a time
+    against the prefill.  Tolerances are those of bf16 storage between the kernels: every
+    stored tensor is half a step off relative to its value, and at most six of them lie
+    between an input and an output, each passed on with a gain below 4."""
+    B, T, D = 2, 70, 128
+    p = make(43, B, T, D, F32, F32, "logit")
+    w = 1.0 + 0.1 * torch.randn(D, generator=torch.Generator().manual_seed(2))
+    x, g, dy = (c(p[k].to(BF)) for k in ("x", "g", "dh"))
+    wd = c(w)
+    n, mean, rstd = la.norm_fwd(x, wd, eps=1e-5)
+    h, last = la.scan_fwd(n, g, gate="logit", tied=True)
+    y, _, r2 = la.norm_fwd(h, wd, kind="rms", eps=1e-5)
+    dh, dw2, _ = la.norm_bwd(dy, h, r2, w=wd, kind="rms", want_db=False)
+    dn, dg, _ = la.scan_bwd(g, h, dh, x=n, gate="logit", tied=True)
+    dx, dw, _ = la.norm_bwd(dn, x, rstd, mean=mean, w=wd, want_db=False)
+
+    X, G, W = (t.double().cpu().requires_grad_() for t in (x, g, wd))
+    m = X.mean(-1, keepdim=True)
+    N = (X - m) / torch.sqrt((X - m).square().mean(-1, keepdim=True) + 1e-5) * W
+    A, s, hs = torch.sigmoid(G), torch.zeros(B, D, dtype=torch.float64), []
+    for t in range(T):
+        s = A[:, t] * s + (1 - A[:, t]) * N[:, t]
+        hs.append(s)
+    H = torch.stack(hs, 1)
+    Y = H / torch.sqrt(H.square().mean(-1, keepdim=True) + 1e-5) * W
+    Y.backward(dy.double().cpu())
+    tol = 6 * 4 * half_step(BF)
+    for got, ref in ((y, Y), (dx, X.grad), (dg, G.grad), (dw + dw2, W.grad)):
+        ref = ref.detach().numpy()
+        assert np.linalg.norm(np64(got) - ref) <= tol * np.linalg.norm(ref)
+    state = torch.zeros(B, D, device="cuda")
+    for t in range(T):
+        nt, _, _ = la.norm_fwd(x[:, t], wd, eps=1e-5)
+        assert torch.equal(nt, n[:, t])
+        ht = la.scan_step(nt, g[:, t], state, gate="logit", tied=True)
+    E, El = fwd_bound(n, g, None, "logit", True)
+    assert np.all(np.abs(np64(state) - np64(last)) <= 2 * El + 1e-37)
+    assert np.all(np.abs(np64(ht) - np64(h[:, -1])) <= 2 * E[:, -1] + 2 * half_step(BF) * np.abs(np64(ht)) + 1e-37)

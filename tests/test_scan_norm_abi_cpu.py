@@ -124,3 +124,16 @@ def test_binding_refuses_cpu_tensors():
         la.norm_fwd(x)
     with pytest.raises(ValueError):
         la.norm_bwd(x, x, x[..., 0], mean=x[..., 0])
+
+
+@pytest.mark.parametrize("make,size", [(fwd, "la_scan_fwd_workspace_size"), (bwd, "la_scan_bwd_workspace_size")])
+def test_scan_workspace(L, make, size):
+    f, n = getattr(L, size), ctypes.c_size_t(7)
+    assert f(None, ctypes.byref(n)) == 1 and f(ctypes.byref(make()), None) == 1
+    assert f(ctypes.byref(make()), ctypes.byref(n)) == 0 and n.value == 0          # short: none
+    assert f(ctypes.byref(make(B=0)), ctypes.byref(n)) == 1
+    assert f(ctypes.byref(make(B=1, T=100000)), ctypes.byref(n)) == 0 and n.value > 0
+    call = L.la_scan_fwd if make is fwd else L.la_scan_bwd
+    for kw in (dict(), dict(workspace=FAKE, workspace_bytes=n.value - 1), dict(workspace=FAKE + 8, workspace_bytes=n.value)):
+        assert call(ctypes.byref(make(B=1, T=100000, **kw)), None) == 8
+    assert call(ctypes.byref(make(T=(1 << 30) + 1)), None) == 2
