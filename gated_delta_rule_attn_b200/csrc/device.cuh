@@ -66,16 +66,29 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
 // One potentially blocking test: the hardware suspends the calling thread until
 // the phase completes or about `kSuspendNs` nanoseconds pass, so waiting warps
 // do not spin on the issue slots and shared-memory pipe that working warps use.
+//
+// CLUSTER (here and in every wait below): acquire at cluster scope, which data that
+// another CTA of the cluster wrote (st.async) needs; the default acquires at CTA scope.
 constexpr uint32_t kSuspendNs = 1000000;
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+            : "memory");
     return ok != 0;
 }
 
@@ -83,15 +96,25 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 constexpr long long kWaitLimitCycles = 2000000000LL;
 
 // Non-blocking test of an mbarrier phase.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 
@@ -104,9 +127,10 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 // kWaitLimitCycles.
 __constant__ long long g_wait_limit = kWaitLimitCycles;
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, long long limit) {
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait<CLUSTER>(bar, parity)) {
         if (clock64() - t0 > limit) {
             raise_error(kErrTimeout);
             return false;
@@ -117,12 +141,13 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, lo
 
 // Bounded wait on an mbarrier phase.  Returns false (and raises kErrTimeout) if
 // the phase did not complete within g_wait_limit cycles.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return true;   // the phase is done: no limit needed
+    if (mbar_test<CLUSTER>(bar, parity)) return true;   // the phase is done: no limit needed
     const long long limit = g_wait_limit;
-    if (limit >= kWaitLimitCycles) return mbar_wait_for(bar, parity, limit);
+    if (limit >= kWaitLimitCycles) return mbar_wait_for<CLUSTER>(bar, parity, limit);
     const long long t0 = clock64();
-    while (!mbar_test(bar, parity)) {
+    while (!mbar_test<CLUSTER>(bar, parity)) {
         if (clock64() - t0 > limit) {
             raise_error(kErrTimeout);
             return false;
@@ -133,9 +158,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
 
 // Wait for asynchronous work this CTA issued (copies, MMAs) before it frees the
 // resources that work uses; bounded by kWaitLimitCycles whatever g_wait_limit is.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_for(bar, parity, kWaitLimitCycles);
+    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
+    return mbar_wait_for<CLUSTER>(bar, parity, kWaitLimitCycles);
 }
 
 // ---------------------------------------------------------------------------

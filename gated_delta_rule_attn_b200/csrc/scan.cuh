@@ -437,13 +437,14 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
     // runs out (the error word is set then), by waits of the full limit from there on.
     int lost = 0;
     uint32_t phases = 0;                       // bit i: the parity of slot i's next arrival
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!lost && mbar_wait(bar, parity)) return;
-        lost = lost < 2 && mbar_drain(bar, parity) ? 1 : 2;
+    auto wait = [&](auto cluster, uint64_t *bar, uint32_t parity) {
+        constexpr bool C = decltype(cluster)::value;
+        if (!lost && mbar_wait<C>(bar, parity)) return;
+        lost = lost < 2 && mbar_drain<C>(bar, parity) ? 1 : 2;
     };
     auto arrived = [&](int slot) {
         if constexpr (VEC) {
-            wait(&full[slot], phases >> slot & 1u);
+            wait(std::false_type{}, &full[slot], phases >> slot & 1u);
             phases ^= 1u << slot;
         } else {
             asm volatile("cp.async.wait_group %0;" ::"n"(kScanStages - 1) : "memory");
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
                         st_async_f4(smem_u32(&cmap[(q * K + rank) * 32]), smem_u32(&heard[q]), (uint32_t)warp,
                                     make_float4(c.A.x, c.A.y, c.X.x, c.X.y));
                     }
-                    wait(&heard[q], parity);
+                    wait(std::true_type{}, &heard[q], parity);   // the maps come from the cluster's CTAs
                     for (int i = 0; i < K; ++i) {
                         if (i == rank) h = carry;
                         map_apply(map_load(&cmap[(q * K + i) * 32]), carry);
