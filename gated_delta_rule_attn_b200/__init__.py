@@ -400,12 +400,14 @@ class _On:
         return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        try:
+            if self.stream is not None:
+                for t in self.tensors:
+                    if isinstance(t, torch.Tensor) and t.device == self.device:   # (a refused one may be elsewhere)
+                        t.record_stream(self.stream)
+        finally:                           # whatever was refused, the caller's stream is current again
+            if self.ctx is not None:
+                self.ctx.__exit__(*exc)
         return False
 
 
