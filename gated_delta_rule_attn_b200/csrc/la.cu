@@ -157,6 +157,38 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// ---------------------------------------------------------------------------
+// The current context, through the driver's entry points.
+// ---------------------------------------------------------------------------
+using PfnCtxGetCurrent = CUresult (*)(CUcontext *);
+using PfnCtxGetId = CUresult (*)(CUcontext, unsigned long long *);
+
+void *driver_fn(const char *name) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return p;
+}
+
+// ID of the calling thread's current CUDA context (false if it cannot be read, and
+// where none is current yet: the runtime binds the primary one lazily).  The driver never
+// gives an ID twice within a process, so what is kept under one is never taken for that of
+// a context made later (after cudaDeviceReset, or by the caller).
+bool current_context_id(unsigned long long *id) {
+    static PfnCtxGetCurrent get_current = nullptr;
+    static PfnCtxGetId get_id = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        get_current = reinterpret_cast<PfnCtxGetCurrent>(driver_fn("cuCtxGetCurrent"));
+        get_id = reinterpret_cast<PfnCtxGetId>(driver_fn("cuCtxGetId"));
+    });
+    CUcontext ctx = nullptr;
+    return get_current && get_id && get_current(&ctx) == CUDA_SUCCESS && ctx &&
+           get_id(ctx, id) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 namespace la {
@@ -190,28 +222,33 @@ bool make_map_4d(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, 
     return r == CUDA_SUCCESS;
 }
 
-// Opt a kernel into more than 48 KB of dynamic shared memory (once per process
-// and device is enough; repeating it is harmless).
 // Opt the kernel in to `bytes` of dynamic shared memory and ask for the largest
 // shared-memory carveout, so that several CTAs of a small-footprint kernel can
 // be resident on one SM (and the occupancy query counts them).
-// Asked of the runtime once per kernel, device and size: the two calls take longer than
-// a launch of few rows.
+// Asked of the runtime once per kernel, context and size: the two calls take longer than
+// a launch of few rows.  A context has its own copy of the kernel, with limits of its own.
+// Where the context cannot be named the runtime is asked every time.
+constexpr size_t kSmemKept = 4096;         // entries; a process of ever new contexts starts again there
 cudaError_t allow_smem(const void *kernel, int bytes) {
     static std::mutex lock;
-    static std::map<std::pair<const void *, int>, int> allowed;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
+    static std::map<std::pair<const void *, unsigned long long>, int> allowed;
+    unsigned long long ctx = 0;
+    const bool named = current_context_id(&ctx);
+    cudaError_t e = cudaSuccess;
     try {
         std::lock_guard<std::mutex> hold(lock);
-        const auto at = allowed.find({kernel, dev});
-        if (at != allowed.end() && at->second >= bytes) return cudaSuccess;
+        if (named) {
+            const auto at = allowed.find({kernel, ctx});
+            if (at != allowed.end() && at->second >= bytes) return cudaSuccess;
+        }
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      (int)cudaSharedmemCarveoutMaxShared);
-        if (e == cudaSuccess) allowed[{kernel, dev}] = bytes;
+        if (e == cudaSuccess && named) {
+            if (allowed.size() >= kSmemKept) allowed.clear();
+            allowed[{kernel, ctx}] = bytes;
+        }
     } catch (const std::bad_alloc &) {
         e = cudaErrorMemoryAllocation;
     }
@@ -380,32 +417,6 @@ struct NoallocEntry {
 };
 NoallocEntry g_noalloc_cache[kNoallocCache];
 int g_noalloc_used = 0, g_noalloc_next = 0;
-
-using PfnCtxGetCurrent = CUresult (*)(CUcontext *);
-using PfnCtxGetId = CUresult (*)(CUcontext, unsigned long long *);
-
-void *driver_fn(const char *name) {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return p;
-}
-
-// ID of the calling thread's current context (false if it cannot be read).
-bool current_context_id(unsigned long long *id) {
-    static PfnCtxGetCurrent get_current = nullptr;
-    static PfnCtxGetId get_id = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        get_current = reinterpret_cast<PfnCtxGetCurrent>(driver_fn("cuCtxGetCurrent"));
-        get_id = reinterpret_cast<PfnCtxGetId>(driver_fn("cuCtxGetId"));
-    });
-    CUcontext ctx = nullptr;
-    return get_current && get_id && get_current(&ctx) == CUDA_SUCCESS && ctx &&
-           get_id(ctx, id) == CUDA_SUCCESS;
-}
 
 la_status noalloc_scratch(void **out) {
     // no context current yet (the runtime binds the primary one lazily): the
