@@ -165,6 +165,17 @@ __device__ __forceinline__ ScanMap map_after(const ScanMap &m, const ScanMap &p)
     if (map_resets(m)) return m;
     return ScanMap{map_resets(p) ? p.A : mul2(m.A, p.A), fma2(m.A, p.X, m.X)};
 }
+// The product of two gates, or gate products, that is 0 only if one of them is: one that
+// underflows keeps its sign and the smallest magnitude there is, so that a map made of many
+// small gates passes an infinite state on as they do one after the other (0 would make it
+// NaN).  A finite state is moved by at most 2^-149 times its size, as by any rounding there.
+// Where factors are many the plain product is taken, and this one if that is 0.
+__device__ __forceinline__ float mul_kept(float a, float b) {
+    const float p = a * b;
+    return p == 0.f && a != 0.f && b != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+__device__ __forceinline__ float2 mul2_kept(float2 a, float2 b) { return make_float2(mul_kept(a.x, b.x), mul_kept(a.y, b.y)); }
+__device__ __forceinline__ bool any_zero(float2 a) { return a.x == 0.f || a.y == 0.f; }
 __device__ __forceinline__ void scan_load(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int c, int row) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
                  ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(row) : "memory");
@@ -212,6 +223,25 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void put_pair(T *p, float2 v, bool ok0, bool ok1) {
     if (ok0) p[0] = from_f32<T>(v.x);
     if (ok1) p[VEC ? 1 : 32] = from_f32<T>(v.y);
+}
+
+// Products with mul2_kept of what the plain product made 0: of the n gates at `at`, `down` apart,
+// and of n maps' products.  Calls, so that they take no registers where they are not made
+// (in line the forward teams spilled: 57.0 against 55.5 us at B=2, T=8192, D=2048).
+template <typename TG, bool VEC, bool LOGIT>
+__device__ __noinline__ float2 gates_kept(uint32_t at, int down, int n) {
+    float2 A = make_float2(1.f, 1.f);
+    for (; n > 0; --n, at += down) {
+        float2 a, r;
+        gate<LOGIT>(take_pair<TG, VEC>(at), a, r);
+        A = mul2_kept(A, a);
+    }
+    return A;
+}
+__device__ __noinline__ float2 maps_kept(const float4 *maps, int n) {
+    float2 A = map_load(maps).A;
+    for (int w = 1; w < n; ++w) A = mul2_kept(A, map_load(maps + w * 32).A);
+    return A;
 }
 
 // Rows that TMA cannot take: a warp copies the n <= R tokens of its own run, channel
@@ -458,8 +488,11 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
     const uint32_t ox = (BWD ? R - 1 : 0) * kScanCB * (uint32_t)sizeof(TX) + lane_off<TX, VEC>();
     int slot = 0;
 
-    // The map m followed by those of the places [rb, r1) of the step in a slot; `starts`: where
-    // sequences start, from the states that `from` gives.
+    // (a 1 that the compiler does not know, so that every gate passes through a product)
+    float one;
+    asm volatile("mov.f32 %0, 0f3F800000;" : "=f"(one));
+    // The map m, whose gate product is 1, followed by those of the places [rb, r1) of the step in a
+    // slot; `starts`: where sequences start, from the states that `from` gives.
     auto compose = [&](ScanMap &m, int slot, int rb, int r1, uint32_t starts, auto from) {
         const uint32_t ag = ring + slot * Shape::kSlot + og;
         const uint32_t au = ring + slot * Shape::kSlot + (BWD ? Shape::kAtD : Shape::kAtX) + ox;
@@ -491,10 +524,9 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
                 }
             }
         }
+        // (a gate of 0, or gates of less than 2^-9 on average)
+        if (!starts && any_zero(m.A)) m.A = gates_kept<TG, VEC, LOGIT>(ag + rb * kGR, kGR, r1 - rb);
     };
-    // (a 1 that the compiler does not know, so that every gate passes through a product)
-    float one;
-    asm volatile("mov.f32 %0, 0f3F800000;" : "=f"(one));
     const float2 zero = make_float2(0.f, 0.f), reset = make_float2(__uint_as_float(kScanReset), __uint_as_float(kScanReset));
 
     if constexpr (MAP) {
@@ -503,7 +535,9 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
         for (int k = 0; k < count; ++k) {
             arrived(slot);
             const int t = origin + k * R;
-            compose(m, slot, max(lo - t, 0), min(R, hi - t), 0u, [&](int) { return zero; });
+            ScanMap step{make_float2(one, one), m.X};
+            compose(step, slot, max(lo - t, 0), min(R, hi - t), 0u, [&](int) { return zero; });
+            m = ScanMap{mul2_kept(m.A, step.A), step.X};
             __syncwarp();
             fetch(k + NS, slot);
             slot = slot + 1 == NS ? 0 : slot + 1;
@@ -571,6 +605,7 @@ __global__ void __launch_bounds__(kScanW * 32 * (MODE == kScanTeam ? 2 : 1)) sca
                         ScanMap c = map_load(wm);
 #pragma unroll 4
                         for (int w = 1; w < W; ++w) c = map_after(map_load(wm + w * 32), c);
+                        if (any_zero(c.A)) c.A = maps_kept(wm, W);   // (a map that forgets has a NaN there)
                         st_async_f4(smem_u32(&cmap[(q * K + rank) * 32]), smem_u32(&heard[q]), (uint32_t)warp,
                                     make_float4(c.A.x, c.A.y, c.X.x, c.X.y));
                     }

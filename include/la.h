@@ -305,7 +305,9 @@ la_status la_fwd_noalloc(const la_fwd_args *args, void *stream);
  *   tied   0: u_t = x_t;  1: u_t = (1 - a_t) x_t.
  * The state, the products and every sum are fp32, whatever the types of x and g;
  * outputs are rounded once.  A NaN or an infinity affects its channel from its
- * token on, as in the formula.
+ * token on, as in the formula: an infinity stays one (of the gates' sign) until a
+ * gate of 0 makes it NaN, however far it is carried.  A logit below -87.3 is a gate
+ * of 0, one above 87.3 a gate of 1 whose 1 - a is 0.
  *
  * Layout (differences from the conventions above are stated here)
  *   - Token tensors are [B,T,D]; a [B,T,H,d] tensor is D = H d.  The channels of a
