@@ -6,16 +6,19 @@
 //     dx = rstd (d - mean(d) - xh mean(d xh))      (rms: without mean(d))
 //     dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// HBM-bound: the forward pass reads and writes every row once, the backward pass
+// Bytes: the forward pass reads and writes every row once, the backward pass
 // reads x and dy and writes dx once.  A row is held in registers by a team of
-// threads, 16 elements a thread: up to 32 threads of one warp for rows of up to
-// 512 (several teams a warp), else the whole CTA.  CTAs walk over rows; each thread
-// copies its own elements of the next rows into its own slots of shared memory
-// (cp.async, no barrier), kNormStages rows ahead, so that enough bytes are in flight
-// whatever the reduction of the current row waits for.  The variance is taken from
-// the centred values, not from a difference of moments.  Measured, bf16 layer norm:
+// threads: 16 elements a thread and up to 32 threads of one warp for rows of up to
+// 512 (several teams a warp), else the whole CTA; forward, rows of more than 512 take
+// 32 elements a thread, one warp up to 1024 and the CTA above.  CTAs walk over rows;
+// each thread copies its own elements of the next rows into its own slots of shared
+// memory (cp.async, no barrier), up to kNormStages rows ahead, so that enough bytes are
+// in flight whatever the reduction of the current row waits for.  The variance is taken
+// from the centred values, not from a difference of moments.  Measured, bf16 layer norm:
 // forward 16384 x 4096 53 us (5.0 TB/s), backward 94 us (4.3 TB/s), backward of RMS
-// rows 262144 x 128 41 us (4.9 TB/s); issue-bound at 16 warps an SM.
+// rows 262144 x 128 41 us (4.9 TB/s).  With 8 to 16 warps an SM (the registers allow no
+// more) what is left is the latency of a row's dependent steps: sums over lanes, barrier,
+// sums over warps; schedulers issue in 54 to 65% of the cycles, DRAM is at 49 to 58%.
 //
 // The weight's gradients are summed without atomics, in an order that does not
 // depend on timing: a thread adds its columns over the rows it meets (fp32), the
@@ -467,6 +470,13 @@ inline NormPlan norm_plan(int64_t R, int D, int per_sm, int e) {
     n.ctas = (int)std::min<int64_t>((R + rows - 1) / rows, resident);
     return n;
 }
+// The threads of an SM that the grids are made for.  They are what the 16-byte forms of bf16
+// rows were fastest with, not what fits.  Fewer are resident, and the rest of the CTAs follow
+// as those end: of the narrow forward pass (95 to 175 registers) one or two CTAs of the four;
+// of the narrow backward pass one of the two where it takes more than 128 registers (all but
+// bf16 in 16 bytes, 124).  Backward with kNormLong threads leaves 64 registers a thread and
+// spills 116 to 680 bytes: 4096 x 16384 takes 146 us in bf16 and 249 in fp32, where the bytes
+// take 61 and 123.
 constexpr int kNormFwdPerSM = 1024, kNormFwdLongPerSM = 384, kNormBwdPerSM = 512;
 // Forward: 32 elements a thread for rows of more than 512, so that few warps meet at the
 // row's two barriers.
@@ -505,7 +515,9 @@ cudaError_t launch_norm_rows(NormParams p, const NormPlan &n, cudaStream_t st) {
 }
 
 // 16-byte accesses where the row length, every row stride and every pointer allow
-// them, else (bf16) 4-byte ones, else single elements.
+// them, else (bf16) 4-byte ones, else single elements.  Layer norm of 16384 bf16 rows,
+// forward and backward: of 4096 elements 53 and 94 us, of 4098 183 and 309, of 4097 590 and
+// 375 (single elements of bf16 come by plain loads, and the wide forms spill).
 template <bool BWD, typename T>
 cudaError_t launch_norm_typed(const NormParams &p, bool layer, const NormPlan &n, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T), V2 = 4 / sizeof(T);

@@ -34,9 +34,9 @@
 // as one: at a sequence's first token the map forgets the state before it
 // (kScanReset), so the load does not depend on the lengths.
 // The order of all sums is fixed: results are the same from run to run.
-// Measured (bf16): forward B=2 T=8192 D=2048, fp32 gates, 55 us (4.9 TB/s of what it
-// cannot do without); backward B=4 T=8192 D=4096 309 us (6.1 TB/s); T=32768 D=1024 with
-// tied logits 68 us forward and 94 us backward (3.0 and 4.3 TB/s).
+// Measured (bf16): forward B=2 T=8192 D=2048, fp32 gates, 56 us (4.8 TB/s of what it
+// cannot do without); backward B=4 T=8192 D=4096 310 to 318 us (6.0 TB/s); T=32768 D=1024
+// with tied logits 68 us forward and 95 us backward (3.0 and 4.2 TB/s).
 #pragma once
 
 #include <algorithm>
@@ -76,7 +76,7 @@ struct ScanTiles {
     CUtensorMap g, x, dh, hs, dx, dg, h;   // boxes of kScanR tokens
 };
 
-constexpr int kScanCB = 64;         // channels per CTA: two a lane
+constexpr int kScanCB = 64;         // channels of a warp, two a lane (a team's warps share them)
 constexpr int kScanR = 16;          // tokens a step
 constexpr int kScanStages = 3;      // slots of a warp (more where warps are few)
 constexpr int kScanMaxStages = 8;
@@ -117,8 +117,11 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
-// a and r = 1 - a of a gate or of its logit.  Of a logit both to full relative
-// accuracy: the exponential is taken of -|l|, so neither overflows nor cancels.
+// a and r = 1 - a of a gate or of its logit l.  The exponential of a logit is taken of -|l|,
+// so neither overflows nor cancels.  The larger of the two is good to 4 half steps of fp32,
+// the smaller to 12 + 2.4 |l| of them (the exponential's documented 2 + 1.2 |l| steps and the
+// quotient's; measured 3 at 0, 16 at 20, 64 at 87); from |l| = 87.34 on, where the exponential
+// is flushed, it is 0.
 template <bool LOGIT>
 __device__ __forceinline__ void gate(float g, float &a, float &r) {
     if (!LOGIT) {
@@ -751,13 +754,21 @@ cudaError_t allow_smem(const void *kernel, int bytes);   // la.cu
 
 // How a call is cut: dense sequences each by themselves or, where they are short, all in
 // one walk; packed ones in one walk.  How a walk is divided is said at the top.
-// Measured (us; bf16 x, fp32 gates unless said):
+// Measured when the borders were chosen (us; bf16 x, fp32 gates unless said):
 //   64 blocks   fwd, B=2 T=8192 D=2048    team of 4 CTAs x 8 warps 59, of 4 x 4 76, two kernels 79
 //   256 blocks  bwd, B=4 T=8192 D=4096    team of 1 CTA x 4 warps 314, a warp each 371, two kernels 413
 //   32 blocks   bwd, packed, T=16384 D=2048   two kernels 117, team of 4 CTAs x 8 warps 179
 //   16 blocks   fwd, T=32768 D=1024, bf16 logits   two kernels 74, team of 8 CTAs x 8 warps 154
-constexpr int kScanShort = 512;     // tokens: below, one warp takes the walk
-constexpr int kScanMany = 296;      // channel blocks: from there on too
+// and around kScanFew in one run, B=1 T=16384 (two kernels / team of 4 CTAs):
+//   blocks                    24         32         48         63         64
+//   fwd                    62 / 80    78 / 80   114 / 97   148 / 98   147 / 99
+//   bwd                    88 / 131  116 / 133  171 / 160  222 / 164  222 / 165
+//   fwd, tied bf16 logits  54 / 111   65 / 111   92 / 150  121 / 154  122 / 154
+//   bwd, tied bf16 logits  73 / 195   95 / 197  143 / 217  190 / 221  190 / 222
+// Values favour the team from about 40 blocks on, tied logits (sigmoids beside the exchange)
+// two kernels at 64 too, and so does T=2048 (by 2 to 7 us): one border for all is a compromise.
+constexpr int kScanShort = 512;     // tokens: up to there one warp takes the walk
+constexpr int kScanMany = 296;      // channel blocks (two for each SM): from there on too
 constexpr int kScanFew = 64;        // channel blocks: below, two kernels
 constexpr int64_t kScanMaxS = 512;  // segments: their maps are applied one after the other
 struct ScanPlan {
@@ -780,7 +791,9 @@ inline ScanPlan scan_plan(const ScanParams &p, int elem, bool vec) {
     int64_t S = 1;
     if (len > kScanShort && q.nblk < kScanMany) {
         if (vec && q.nblk >= kScanFew) {
-            // two CTAs an SM
+            // as many CTAs as two an SM make.  (A tied backward pass of fp32 x takes 123 to 139 KB
+            // a CTA, so there one fits and some of the CTAs wait for a second turn: B=2 T=8192
+            // D=2048 188 us where the bytes take 123.)
             q.K = q.nblk * 4 <= 2 * sm_count() ? 4 : q.nblk * 2 <= 2 * sm_count() ? 2 : 1;
             q.W = elem <= 6 ? 2 * kScanW : kScanW;
             q.NS = 2;

@@ -415,7 +415,9 @@ la_status la_scan_fwd(const la_scan_fwd_args *args, void *stream);
 la_status la_scan_bwd(const la_scan_bwd_args *args, void *stream);
 la_status la_scan_step(const la_scan_step_args *args, void *stream);
 
-/* Scratch of a call; reads the types, tied, B, T, D and whether cu_seqlens is NULL. */
+/* Scratch of a call; it depends on the types, tied, B, T, D and whether cu_seqlens is
+ * NULL.  Types, gate, tied, sizes, max_seqlen and the alignment of cu_seqlens are checked
+ * as in the call; other fields are not read. */
 la_status la_scan_fwd_workspace_size(const la_scan_fwd_args *args, size_t *bytes);
 la_status la_scan_bwd_workspace_size(const la_scan_bwd_args *args, size_t *bytes);
 
@@ -425,7 +427,9 @@ la_status la_scan_bwd_workspace_size(const la_scan_bwd_args *args, size_t *bytes
  *     LA_NORM_RMS    xh = x rstd,           rstd = 1 / sqrt(mean(x^2) + eps)
  *     y = xh w + b
  * The head-wise RMS normalisation of la_fwd's out_norm is LA_NORM_RMS over
- * R = B T H rows of D = dv.  Gradients, with d = dy w:
+ * R = B T H rows of D = dv; out_norm works in place and keeps no statistics, so
+ * inference takes it and training this call, which leaves rstd for the gradients.
+ * Gradients, with d = dy w:
  *     dx = rstd (d - mean(d) - xh mean(d xh))   (RMS: without mean(d)),
  *     dw = sum over rows of dy xh,  db = sum over rows of dy.
  * x, y, dy, dx [R,D] of `dtype`, elements of a row contiguous, `*_row` elements
@@ -433,7 +437,8 @@ la_status la_scan_bwd_workspace_size(const la_scan_bwd_args *args, size_t *bytes
  * [R] fp32.  w NULL means 1, b NULL means 0.  Statistics and sums are fp32, outputs
  * are rounded once, and the gradients' sums have a fixed order.  Pointers need the
  * alignment of their element; 16-byte accesses are used where D, the strides and
- * the pointers allow them, else single elements.  eps > 0 (finite).
+ * the pointers allow them, else for bf16 4-byte ones, else single elements (up to 11
+ * times slower for long bf16 rows).  eps > 0 (finite).
  * la_norm_fwd writes mean (layer only) and rstd where they are not NULL;
  * la_norm_bwd reads them (mean: layer only).  dw and db may each be NULL.  R == 0
  * gives zero dw and db.
@@ -481,7 +486,8 @@ typedef struct la_norm_bwd_args {
     size_t workspace_bytes;
 } la_norm_bwd_args;
 
-/* Asynchronous on `stream`; the size query reads R, D, dw and db only. */
+/* Asynchronous on `stream`; the size depends on R, D and on whether dw and db are
+ * NULL (the query checks the types, kind and sizes as the call does). */
 la_status la_norm_fwd(const la_norm_fwd_args *args, void *stream);
 la_status la_norm_bwd(const la_norm_bwd_args *args, void *stream);
 la_status la_norm_bwd_workspace_size(const la_norm_bwd_args *args, size_t *bytes);
